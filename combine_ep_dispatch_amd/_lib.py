@@ -16,9 +16,18 @@ EP_ERR_HIP = 3
 
 EP_RECV_FP8_E4M3_G128 = 0
 EP_RECV_BF16 = 1
+EP_RECV_MXFP4_G32 = 2
+
+EP_DTYPE_F32 = 0
+EP_DTYPE_BF16 = 1
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
+EP_ACT_NONE = 0
+EP_ACT_SWIGLU = 1
 
 EP_MAX_EXPERTS = 1024
 EP_MAX_TOPK = 32
+EP_MAX_GROUPS = 64
 EP_NOALLOC_SCRATCH_BYTES = 1 << 20
 
 # ep_step_plan: opaque caller-owned storage of 32 uint64
@@ -41,6 +50,11 @@ EXPORTS = (
     "ep_step_plan_combine",
     "ep_dispatch_backward",
     "ep_combine_backward",
+    "ep_route",
+    "ep_route_backward",
+    "ep_quantize_rows",
+    "ep_dequantize_rows",
+    "ep_expert_product",
     "ep_cast_fp8_e4m3",
 )
 
@@ -91,6 +105,17 @@ def _load():
     lib.ep_dispatch_backward.restype = ctypes.c_int
     lib.ep_combine_backward.argtypes = [p, p, p, p, i64, i32, i32, p, p, p]
     lib.ep_combine_backward.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.ep_route.argtypes = [p, i32, p, i64, i32, i32, i32, i32, i32, i32, f32, p, p, p]
+    lib.ep_route.restype = ctypes.c_int
+    lib.ep_route_backward.argtypes = [p, p, i32, p, i64, i32, i32, i32, i32, f32, p, p]
+    lib.ep_route_backward.restype = ctypes.c_int
+    lib.ep_quantize_rows.argtypes = [p, i64, i32, i32, p, p, p]
+    lib.ep_quantize_rows.restype = ctypes.c_int
+    lib.ep_dequantize_rows.argtypes = [p, p, i64, i32, i32, p, p]
+    lib.ep_dequantize_rows.restype = ctypes.c_int
+    lib.ep_expert_product.argtypes = [p, p, i32, p, p, p, i64, i32, i32, i32, i32, i32, p, p]
+    lib.ep_expert_product.restype = ctypes.c_int
     lib.ep_cast_fp8_e4m3.argtypes = [p, p, i64, p]
     lib.ep_cast_fp8_e4m3.restype = ctypes.c_int
     return lib

@@ -16,7 +16,8 @@ from collections import namedtuple
 
 import torch
 
-from ._lib import (EP_MAX_EXPERTS, EP_MAX_TOPK, EP_RECV_BF16, EP_RECV_FP8_E4M3_G128, LIB, check)
+from ._lib import (EP_ACT_NONE, EP_ACT_SWIGLU, EP_DTYPE_BF16, EP_DTYPE_F32, EP_MAX_EXPERTS, EP_MAX_TOPK,
+                   EP_RECV_BF16, EP_RECV_FP8_E4M3_G128, EP_RECV_MXFP4_G32, EP_SCORE_SIGMOID, LIB, check)
 
 Handle = namedtuple("Handle", "tokens_per_expert expert_offset slot src_token num_experts")
 # low-latency (padded) handle: expert e owns rows e*capacity .. e*capacity+capacity-1
@@ -64,6 +65,53 @@ _IDX = (torch.int32, torch.int64)  # expert ids: int32, or int64 as routers prod
 _F32 = (torch.float32,)
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _U8 = (torch.uint8, torch.float8_e4m3fn)
+_BYTES = (torch.uint8,)
+
+
+def _need_recv(format, recv_x, recv_scale, R, H, names=("recv_x", "recv_scale")):
+    """Shapes and types of R rows of H channels in a receive format."""
+    if format == EP_RECV_FP8_E4M3_G128:
+        if H % 128:
+            raise ValueError("FP8 dispatch needs hidden % 128 == 0")
+        _need(recv_x, names[0], _U8, (R, H))
+        _need(recv_scale, names[1], _F32, (R, H // 128))
+    elif format == EP_RECV_MXFP4_G32:
+        if H % 32:
+            raise ValueError("MXFP4 rows need hidden % 32 == 0")
+        _need(recv_x, names[0], _BYTES, (R, H // 2))
+        _need(recv_scale, names[1], _BYTES, (R, H // 32))
+    elif format == EP_RECV_BF16:
+        _need(recv_x, names[0], _BF16, (R, H))
+    else:
+        raise ValueError("unknown receive format %r" % (format,))
+
+
+def _new_recv(format, R, H, dev):
+    """Receive buffers of R rows: (recv_x, recv_scale or None)."""
+    if format == EP_RECV_FP8_E4M3_G128:
+        return (torch.empty((R, H), dtype=torch.uint8, device=dev),
+                torch.empty((R, H // 128), dtype=torch.float32, device=dev))
+    if format == EP_RECV_MXFP4_G32:
+        return (torch.empty((R, H // 2), dtype=torch.uint8, device=dev),
+                torch.empty((R, H // 32), dtype=torch.uint8, device=dev))
+    if format == EP_RECV_BF16:
+        return torch.empty((R, H), dtype=torch.bfloat16, device=dev), None
+    raise ValueError("unknown receive format %r" % (format,))
+
+
+def _format(fp8, format):
+    """The receive format: ``format`` where it is given, else by the fp8 flag."""
+    if format is not None:
+        return int(format)
+    return EP_RECV_FP8_E4M3_G128 if fp8 else EP_RECV_BF16
+
+
+def _same_device(first, *others):
+    """The operands' one device; launches go to that device's current stream."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("operands on different devices: %s and %s" % (first.device, t.device))
+    return first.device
 
 
 def _ids_fn(name, topk_idx):
@@ -141,6 +189,8 @@ def ep_dispatch(x, slot, topk_weights, format, recv_x, recv_scale=None, recv_wei
     """Copy every token x [T, H] (bf16) into its K receive rows given by slot:
     EP_RECV_FP8_E4M3_G128 writes E4M3FN codes to recv_x (uint8 [rows, H])
     and one float32 scale per 128 channels to recv_scale [rows, H/128];
+    EP_RECV_MXFP4_G32 writes E2M1 codes (uint8 [rows, H/2], the even channel
+    in the low half) and one scale byte per 32 channels (uint8 [rows, H/32]);
     EP_RECV_BF16 copies the bf16 bits to recv_x (bf16 [rows, H]).
     recv_weight [rows] (optional) receives topk_weights[t, k].  num_rows:
     rows of the receive buffers (T*K by default; E*capacity for a padded
@@ -156,15 +206,7 @@ def ep_dispatch(x, slot, topk_weights, format, recv_x, recv_scale=None, recv_wei
     R = T * K if num_rows is None else int(num_rows)
     if topk_weights is not None:
         _need(topk_weights, "topk_weights", _F32, (T, K))
-    if format == EP_RECV_FP8_E4M3_G128:
-        _need(recv_x, "recv_x", _U8, (R, H))
-        if H % 128:
-            raise ValueError("FP8 dispatch needs hidden % 128 == 0")
-        _need(recv_scale, "recv_scale", _F32, (R, H // 128))
-    elif format == EP_RECV_BF16:
-        _need(recv_x, "recv_x", _BF16, (R, H))
-    else:
-        raise ValueError("unknown receive format %r" % (format,))
+    _need_recv(format, recv_x, recv_scale, R, H)
     if recv_weight is not None:
         _need(recv_weight, "recv_weight", _F32, (R,))
     check("ep_dispatch", LIB.ep_dispatch(
@@ -199,15 +241,7 @@ def _check_layout_dispatch(topk_idx, x, topk_weights, num_experts, capacity, for
     _need(src_token, "src_token", _I32, (R,))
     if topk_weights is not None:
         _need(topk_weights, "topk_weights", _F32, (T, K))
-    if format == EP_RECV_FP8_E4M3_G128:
-        if H % 128:
-            raise ValueError("FP8 dispatch needs hidden % 128 == 0")
-        _need(recv_x, "recv_x", _U8, (R, H))
-        _need(recv_scale, "recv_scale", _F32, (R, H // 128))
-    elif format == EP_RECV_BF16:
-        _need(recv_x, "recv_x", _BF16, (R, H))
-    else:
-        raise ValueError("unknown receive format %r" % (format,))
+    _need_recv(format, recv_x, recv_scale, R, H)
     if recv_weight is not None:
         _need(recv_weight, "recv_weight", _F32, (R,))
     return T, H, K
@@ -312,6 +346,123 @@ def ep_combine_backward(grad_out, y, slot, topk_weights, grad_y, grad_w=None, st
         T, H, K, grad_y.data_ptr(), grad_w.data_ptr() if grad_w is not None else None, _stream(stream)))
 
 
+def _logits_dtype(logits):
+    return EP_DTYPE_BF16 if logits.dtype == torch.bfloat16 else EP_DTYPE_F32
+
+
+_LOGITS = (torch.float32, torch.bfloat16)
+
+
+def ep_route(logits, bias, n_group, topk_group, score, renormalize, scale, topk_idx, topk_weights, stream=None):
+    """Router logits [T, E] (float32 or bf16) to topk_idx (int32 [T, K], by
+    descending score, -1 where no expert is left) and topk_weights (float32
+    [T, K]).  score: EP_SCORE_SIGMOID or EP_SCORE_SOFTMAX; bias (float32 [E]
+    or None) is added to the scores for the choice only; the topk_group best
+    of n_group groups are kept; renormalize divides by the sum of the chosen
+    scores; scale multiplies the weights."""
+    _need(logits, "logits", _LOGITS)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, "bias", _F32, (E,))
+    _need(topk_idx, "topk_idx", _I32)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError("topk_idx must be [T, K]")
+    K = topk_idx.shape[1]
+    _need(topk_weights, "topk_weights", _F32, (T, K))
+    with torch.cuda.device(_same_device(logits, bias, topk_idx, topk_weights)):
+        check("ep_route", LIB.ep_route(
+            logits.data_ptr(), _logits_dtype(logits), bias.data_ptr() if bias is not None else None, T, E, K,
+            int(n_group), int(topk_group), int(score), int(bool(renormalize)), float(scale), topk_idx.data_ptr(),
+            topk_weights.data_ptr(), _stream(stream)))
+
+
+def ep_route_backward(grad_w, logits, topk_idx, score, renormalize, scale, grad_logits, stream=None):
+    """Gradient of ep_route's weights: grad_w float32 [T, K] to grad_logits
+    [T, E], of the logits' type.  Entries of topk_idx outside [0, E) count
+    for nothing."""
+    _need(logits, "logits", _LOGITS)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    _need(topk_idx, "topk_idx", _I32)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError("topk_idx must be [T, K]")
+    K = topk_idx.shape[1]
+    _need(grad_w, "grad_w", _F32, (T, K))
+    _need(grad_logits, "grad_logits", (logits.dtype,), (T, E))
+    with torch.cuda.device(_same_device(logits, grad_w, topk_idx, grad_logits)):
+        check("ep_route_backward", LIB.ep_route_backward(
+            grad_w.data_ptr(), logits.data_ptr(), _logits_dtype(logits), topk_idx.data_ptr(), T, E, K, int(score),
+            int(bool(renormalize)), float(scale), grad_logits.data_ptr(), _stream(stream)))
+
+
+def ep_quantize_rows(x, format, q, scale, stream=None):
+    """Rows x [R, H] (bf16) to the codes and scales dispatch would write for
+    them: FP8 (uint8 [R, H], float32 [R, H/128]) or MXFP4 (uint8 [R, H/2],
+    uint8 [R, H/32])."""
+    _need(x, "x", _BF16)
+    if x.dim() != 2:
+        raise ValueError("x must be [R, H]")
+    R, H = x.shape
+    if format not in (EP_RECV_FP8_E4M3_G128, EP_RECV_MXFP4_G32):
+        raise ValueError("rows are quantised to FP8 or MXFP4, not format %r" % (format,))
+    _need_recv(format, q, scale, R, H, ("q", "scale"))
+    with torch.cuda.device(_same_device(x, q, scale)):
+        check("ep_quantize_rows", LIB.ep_quantize_rows(x.data_ptr(), R, H, int(format), q.data_ptr(),
+                                                       scale.data_ptr(), _stream(stream)))
+
+
+def ep_dequantize_rows(q, scale, format, x, stream=None):
+    """The values (bf16 [R, H]) that FP8 or MXFP4 codes and scales stand for."""
+    _need(x, "x", _BF16)
+    if x.dim() != 2:
+        raise ValueError("x must be [R, H]")
+    R, H = x.shape
+    if format not in (EP_RECV_FP8_E4M3_G128, EP_RECV_MXFP4_G32):
+        raise ValueError("rows are dequantised from FP8 or MXFP4, not format %r" % (format,))
+    _need_recv(format, q, scale, R, H, ("q", "scale"))
+    with torch.cuda.device(_same_device(x, q, scale)):
+        check("ep_dequantize_rows", LIB.ep_dequantize_rows(q.data_ptr(), scale.data_ptr(), R, H, int(format),
+                                                           x.data_ptr(), _stream(stream)))
+
+
+def ep_expert_product(a, a_scale, format, w, w_scale, expert_rows, capacity, activation, y, stream=None):
+    """y[r] = act(w[e(r)] @ a[r]) for every expert's rows.  a, a_scale: rows in
+    MXFP4 or FP8 (format EP_RECV_*); w uint8 [E, N, H/2] and w_scale uint8
+    [E, N, H/32]: MXFP4; expert_rows: expert_offset int32 [E+1] (capacity 0)
+    or recv_expert_count int32 [E] (capacity > 0, rows = E*capacity);
+    activation EP_ACT_NONE (y bf16 [rows, N]) or EP_ACT_SWIGLU (y bf16 [rows,
+    N/2]: silu of the first N/2 products times the others).  Rows of no
+    expert are left untouched."""
+    _need(w, "w", _BYTES)
+    if w.dim() != 3:
+        raise ValueError("w must be [E, N, H/2]")
+    E, N, H = w.shape[0], w.shape[1], w.shape[2] * 2
+    if H % 128:
+        raise ValueError("the product needs hidden % 128 == 0")
+    _need(w_scale, "w_scale", _BYTES, (E, N, H // 32))
+    if format not in (EP_RECV_FP8_E4M3_G128, EP_RECV_MXFP4_G32):
+        raise ValueError("the product takes FP8 or MXFP4 rows, not format %r" % (format,))
+    if not isinstance(a, torch.Tensor) or a.dim() != 2:
+        raise ValueError("a must be [rows, bytes of a row]")
+    R, cap = a.shape[0], int(capacity)
+    _need_recv(format, a, a_scale, R, H, ("a", "a_scale"))
+    if cap < 0 or (cap > 0 and R != E * cap):
+        raise ValueError("capacity %d does not fit %d rows of %d experts" % (cap, R, E))
+    _need(expert_rows, "expert_rows", _I32, (E,) if cap else (E + 1,))
+    if activation not in (EP_ACT_NONE, EP_ACT_SWIGLU):
+        raise ValueError("unknown activation %r" % (activation,))
+    if N % (16 if activation == EP_ACT_SWIGLU else 8):
+        raise ValueError("the product needs out channels in multiples of 8")
+    _need(y, "y", _BF16, (R, N // 2 if activation == EP_ACT_SWIGLU else N))
+    with torch.cuda.device(_same_device(a, a_scale, w, w_scale, expert_rows, y)):
+        check("ep_expert_product", LIB.ep_expert_product(
+            a.data_ptr(), a_scale.data_ptr(), int(format), w.data_ptr(), w_scale.data_ptr(), expert_rows.data_ptr(),
+            R, E, cap, H, N, int(activation), y.data_ptr(), _stream(stream)))
+
+
 def ep_cast_fp8_e4m3(inp, out, stream=None):
     """The binary32 -> E4M3FN conversion dispatch uses (round to nearest
     even, saturating at +-448), elementwise: inp float32, out uint8 of the
@@ -342,13 +493,15 @@ def layout(topk_idx, num_experts, stream=None):
     return Handle(counts, offsets, slot, src, E)
 
 
-def dispatch(x, topk_idx, topk_weights, num_experts, fp8=True, handle=None, stream=None):
+def dispatch(x, topk_idx, topk_weights, num_experts, fp8=True, handle=None, stream=None, format=None):
     """Permute tokens into expert-major rows.
 
     Returns (recv_x, recv_scale, recv_weight, handle): recv_x is uint8 E4M3FN
     [T*K, H] with recv_scale float32 [T*K, H/128] when ``fp8``, else bfloat16
     [T*K, H] with recv_scale None; recv_weight float32 [T*K] (None if
-    ``topk_weights`` is None).  Rows expert_offset[e] .. expert_offset[e+1]-1
+    ``topk_weights`` is None).  ``format`` (EP_RECV_*) picks the receive
+    format instead of ``fp8``: EP_RECV_MXFP4_G32 gives uint8 [T*K, H/2] codes
+    and uint8 [T*K, H/32] scales.  Rows expert_offset[e] .. expert_offset[e+1]-1
     belong to expert e.
     """
     T, H = x.shape
@@ -360,13 +513,8 @@ def dispatch(x, topk_idx, topk_weights, num_experts, fp8=True, handle=None, stre
     if topk_weights is not None:
         topk_weights = topk_weights.to(torch.float32).contiguous()
         recv_weight = torch.empty(T * K, dtype=torch.float32, device=dev)
-    fmt = EP_RECV_FP8_E4M3_G128 if fp8 else EP_RECV_BF16
-    if fp8:
-        recv_x = torch.empty((T * K, H), dtype=torch.uint8, device=dev)
-        recv_scale = torch.empty((T * K, H // 128), dtype=torch.float32, device=dev)
-    else:
-        recv_x = torch.empty((T * K, H), dtype=torch.bfloat16, device=dev)
-        recv_scale = None
+    fmt = _format(fp8, format)
+    recv_x, recv_scale = _new_recv(fmt, T * K, H, dev)
     if handle is not None:
         ep_dispatch(x, handle.slot, topk_weights, fmt, recv_x, recv_scale, recv_weight, stream)
         return recv_x, recv_scale, recv_weight, handle
@@ -408,13 +556,15 @@ def layout_padded(topk_idx, num_experts, capacity, stream=None):
     return PaddedHandle(count, slot, src, E, cap)
 
 
-def low_latency_dispatch(x, topk_idx, num_max_tokens, num_experts, fp8=True, stream=None):
+def low_latency_dispatch(x, topk_idx, num_max_tokens, num_experts, fp8=True, stream=None, format=None):
     """Decode-time dispatch into a padded buffer, shaped like the pages'
     ``low_latency_dispatch(hidden_states, topk_idx, num_max_tokens,
     num_experts)`` ([P4] "使用示例 › 推理解码阶段的应用").
 
     Returns (recv_x [E, num_max_tokens, H], recv_scale [E, num_max_tokens,
-    H/128] or None, recv_expert_count [E], handle).
+    H/128] or None, recv_expert_count [E], handle).  ``format`` (EP_RECV_*)
+    picks the receive format instead of ``fp8``; MXFP4 rows have H/2 bytes
+    and H/32 scale bytes.
     """
     topk_idx = _as_ids(topk_idx)
     T, H = x.shape
@@ -428,17 +578,12 @@ def low_latency_dispatch(x, topk_idx, num_max_tokens, num_experts, fp8=True, str
     src = torch.empty(E * cap, dtype=torch.int32, device=dev)
     nb = ep_layout_workspace_bytes(T, K, E)
     ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
-    if fp8:
-        recv_x = torch.empty((E * cap, H), dtype=torch.uint8, device=dev)
-        recv_scale = torch.empty((E * cap, H // 128), dtype=torch.float32, device=dev)
-    else:
-        recv_x = torch.empty((E * cap, H), dtype=torch.bfloat16, device=dev)
-        recv_scale = None
-    ep_layout_dispatch(topk_idx, x, None, E, cap, EP_RECV_FP8_E4M3_G128 if fp8 else EP_RECV_BF16, count, None,
-                       slot, src, recv_x, recv_scale, None, ws, stream)
+    fmt = _format(fp8, format)
+    recv_x, recv_scale = _new_recv(fmt, E * cap, H, dev)
+    ep_layout_dispatch(topk_idx, x, None, E, cap, fmt, count, None, slot, src, recv_x, recv_scale, None, ws, stream)
     if recv_scale is not None:
-        recv_scale = recv_scale.view(E, cap, H // 128)
-    return recv_x.view(E, cap, H), recv_scale, count, PaddedHandle(count, slot, src, E, cap)
+        recv_scale = recv_scale.view(E, cap, -1)
+    return recv_x.view(E, cap, -1), recv_scale, count, PaddedHandle(count, slot, src, E, cap)
 
 
 def low_latency_combine(y, handle, topk_weights, stream=None):
@@ -472,3 +617,57 @@ def combine_backward(grad_out, y, handle, topk_weights, stream=None):
     ep_combine_backward(grad_out, y, handle.slot, topk_weights.to(torch.float32).contiguous(), grad_y, grad_w,
                         stream, num_rows=R)
     return grad_y, grad_w
+
+
+def route(logits, top_k, bias=None, n_group=1, topk_group=1, score=EP_SCORE_SIGMOID, renormalize=True, scale=1.0,
+          stream=None):
+    """Router logits [T, E] -> (topk_idx int32 [T, K], topk_weights float32
+    [T, K]), as dispatch and combine take them (see ep_route)."""
+    T, K = logits.shape[0], int(top_k)
+    if not 1 <= K <= EP_MAX_TOPK:
+        raise ValueError("unsupported top_k=%d" % K)
+    topk_idx = torch.empty((T, K), dtype=torch.int32, device=logits.device)
+    topk_weights = torch.empty((T, K), dtype=torch.float32, device=logits.device)
+    ep_route(logits, bias, n_group, topk_group, score, renormalize, scale, topk_idx, topk_weights, stream)
+    return topk_idx, topk_weights
+
+
+def route_backward(grad_w, logits, topk_idx, score=EP_SCORE_SIGMOID, renormalize=True, scale=1.0, stream=None):
+    """Gradient of route's weights (combine_backward's grad_w) w.r.t. the
+    logits -> [T, E] of their type."""
+    grad_logits = torch.empty_like(logits)
+    ep_route_backward(grad_w, logits, topk_idx, score, renormalize, scale, grad_logits, stream)
+    return grad_logits
+
+
+def quantize_rows(x, format=EP_RECV_MXFP4_G32, stream=None):
+    """Rows x [R, H] (bf16) -> (codes, scales), as dispatch leaves them."""
+    if format not in (EP_RECV_FP8_E4M3_G128, EP_RECV_MXFP4_G32):
+        raise ValueError("rows are quantised to FP8 or MXFP4, not format %r" % (format,))
+    q, scale = _new_recv(format, x.shape[0], x.shape[1], x.device)
+    ep_quantize_rows(x, format, q, scale, stream)
+    return q, scale
+
+
+def dequantize_rows(q, scale, format=EP_RECV_MXFP4_G32, stream=None):
+    """Codes and scales -> the bf16 rows [R, H] they stand for."""
+    H = q.shape[1] * (2 if format == EP_RECV_MXFP4_G32 else 1)
+    x = torch.empty((q.shape[0], H), dtype=torch.bfloat16, device=q.device)
+    ep_dequantize_rows(q, scale, format, x, stream)
+    return x
+
+
+def expert_product(a, a_scale, w, w_scale, handle, activation=EP_ACT_NONE, stream=None):
+    """Every expert's product on its rows -> bf16 [rows, N] (N/2 channels with
+    EP_ACT_SWIGLU), [E, capacity, ..] for a PaddedHandle.  a, a_scale: as
+    dispatch (or low_latency_dispatch) returned them with ``handle``, or
+    quantize_rows made them; uint8 scales mean MXFP4 rows, float32 scales
+    FP8.  Rows of no expert hold no defined values."""
+    format = EP_RECV_MXFP4_G32 if a_scale.dtype == torch.uint8 else EP_RECV_FP8_E4M3_G128
+    padded = isinstance(handle, PaddedHandle)
+    a2, s2 = a.reshape(-1, a.shape[-1]), a_scale.reshape(-1, a_scale.shape[-1])
+    out = w.shape[1] // 2 if activation == EP_ACT_SWIGLU else w.shape[1]
+    y = torch.empty((a2.shape[0], out), dtype=torch.bfloat16, device=a.device)
+    ep_expert_product(a2, s2, format, w, w_scale, handle.recv_expert_count if padded else handle.expert_offset,
+                      handle.capacity if padded else 0, activation, y, stream)
+    return y.view(handle.num_experts, handle.capacity, out) if padded else y

@@ -72,12 +72,14 @@ ep_status check_layout(const void* topk_idx, size_t id_bytes, int64_t T, int32_t
 // Checks of the dispatch arguments other than slot; the buffers are only
 // checked when there are tokens.
 ep_status check_dispatch(const void* x, int64_t T, int32_t H, int32_t K, const float* topk_weights, int32_t format,
-                         const void* recv_x, const float* recv_scale, const float* recv_weight) {
+                         const void* recv_x, const void* recv_scale, const float* recv_weight) {
   ep_status st = check_common(T, K);
   if (st != EP_OK) return st;
   if (H <= 0) return EP_ERR_INVALID_ARG;
-  if (format != EP_RECV_FP8_E4M3_G128 && format != EP_RECV_BF16) return EP_ERR_INVALID_ARG;
+  if (format != EP_RECV_FP8_E4M3_G128 && format != EP_RECV_BF16 && format != EP_RECV_MXFP4_G32)
+    return EP_ERR_INVALID_ARG;
   if (format == EP_RECV_FP8_E4M3_G128 && H % 128 != 0) return EP_ERR_INVALID_ARG;
+  if (format == EP_RECV_MXFP4_G32 && H % 32 != 0) return EP_ERR_INVALID_ARG;
   if (H % 8 != 0) return EP_ERR_INVALID_ARG;
   if (recv_weight != nullptr && topk_weights == nullptr) return EP_ERR_INVALID_ARG;
   if (T * H >= kMaxElems) return EP_ERR_UNSUPPORTED;
@@ -87,6 +89,7 @@ ep_status check_dispatch(const void* x, int64_t T, int32_t H, int32_t K, const f
   if (topk_weights && !aligned(topk_weights, 4)) return EP_ERR_INVALID_ARG;
   if (recv_weight && !aligned(recv_weight, 4)) return EP_ERR_INVALID_ARG;
   if (format == EP_RECV_FP8_E4M3_G128 && (!recv_scale || !aligned(recv_scale, 4))) return EP_ERR_INVALID_ARG;
+  if (format == EP_RECV_MXFP4_G32 && !recv_scale) return EP_ERR_INVALID_ARG;
   return EP_OK;
 }
 
@@ -189,7 +192,7 @@ EP_API ep_status ep_dispatch_layout_padded_i64(const int64_t* topk_idx, int64_t 
 
 EP_API ep_status ep_dispatch(const void* x, int64_t num_tokens, int32_t hidden, int32_t top_k,
                              const int32_t* slot, const float* topk_weights, int32_t format, void* recv_x,
-                             float* recv_scale, float* recv_weight, void* stream) {
+                             void* recv_scale, float* recv_weight, void* stream) {
   ep_status st = check_dispatch(x, num_tokens, hidden, top_k, topk_weights, format, recv_x, recv_scale, recv_weight);
   if (st != EP_OK) return st;
   if (num_tokens == 0) return EP_OK;
@@ -198,8 +201,13 @@ EP_API ep_status ep_dispatch(const void* x, int64_t num_tokens, int32_t hidden, 
   const int32_t T = static_cast<int32_t>(num_tokens);
   if (format == EP_RECV_FP8_E4M3_G128)
     return from_hip(ep::launch_dispatch_fp8(static_cast<const uint16_t*>(x), T, hidden, top_k, slot,
-                                            topk_weights, static_cast<uint8_t*>(recv_x), recv_scale,
+                                            topk_weights, static_cast<uint8_t*>(recv_x),
+                                            static_cast<float*>(recv_scale),
                                             recv_weight, s));
+  if (format == EP_RECV_MXFP4_G32)
+    return from_hip(ep::launch_dispatch_mxfp4(static_cast<const uint16_t*>(x), T, hidden, top_k, slot, topk_weights,
+                                              static_cast<uint8_t*>(recv_x), static_cast<uint8_t*>(recv_scale),
+                                              recv_weight, s));
   return from_hip(ep::launch_dispatch_bf16(static_cast<const uint16_t*>(x), T, hidden, top_k, slot,
                                            topk_weights, static_cast<uint16_t*>(recv_x), recv_weight, s));
 }
@@ -211,7 +219,7 @@ ep_status check_layout_dispatch(const Idx* topk_idx, const void* x, const float*
                                 int32_t hidden, int32_t top_k, int32_t num_experts, int32_t capacity,
                                 int32_t format, const int32_t* tokens_per_expert, const int32_t* expert_offset,
                                 const int32_t* slot, const int32_t* src_token, const void* recv_x,
-                                const float* recv_scale, const float* recv_weight, const void* workspace,
+                                const void* recv_scale, const float* recv_weight, const void* workspace,
                                 size_t workspace_bytes) {
   ep_status st = check_layout(topk_idx, sizeof(Idx), num_tokens, top_k, num_experts, capacity, tokens_per_expert,
                               capacity == 0 ? expert_offset : nullptr, slot, src_token, workspace,
@@ -224,7 +232,7 @@ template <typename Idx>
 ep_status layout_dispatch(const Idx* topk_idx, const void* x, const float* topk_weights, int64_t num_tokens,
                           int32_t hidden, int32_t top_k, int32_t num_experts, int32_t capacity, int32_t format,
                           int32_t* tokens_per_expert, int32_t* expert_offset, int32_t* slot, int32_t* src_token,
-                          void* recv_x, float* recv_scale, float* recv_weight, void* workspace,
+                          void* recv_x, void* recv_scale, float* recv_weight, void* workspace,
                           size_t workspace_bytes, void* stream) {
   const ep_status st = check_layout_dispatch(topk_idx, x, topk_weights, num_tokens, hidden, top_k, num_experts,
                                              capacity, format, tokens_per_expert, expert_offset, slot, src_token,
@@ -232,7 +240,7 @@ ep_status layout_dispatch(const Idx* topk_idx, const void* x, const float* topk_
   if (st != EP_OK) return st;
   return from_hip(ep::launch_layout_dispatch(
       topk_idx, static_cast<const uint16_t*>(x), topk_weights, static_cast<int32_t>(num_tokens), hidden, top_k,
-      num_experts, capacity, format == EP_RECV_FP8_E4M3_G128, tokens_per_expert,
+      num_experts, capacity, format, tokens_per_expert,
       capacity == 0 ? expert_offset : nullptr, slot, src_token, recv_x, recv_scale, recv_weight, workspace,
       static_cast<hipStream_t>(stream)));
 }
@@ -243,7 +251,7 @@ EP_API ep_status ep_layout_dispatch(const int32_t* topk_idx, const void* x, cons
                                     int64_t num_tokens, int32_t hidden, int32_t top_k, int32_t num_experts,
                                     int32_t capacity, int32_t format, int32_t* tokens_per_expert,
                                     int32_t* expert_offset, int32_t* slot, int32_t* src_token, void* recv_x,
-                                    float* recv_scale, float* recv_weight, void* workspace,
+                                    void* recv_scale, float* recv_weight, void* workspace,
                                     size_t workspace_bytes, void* stream) {
   return layout_dispatch(topk_idx, x, topk_weights, num_tokens, hidden, top_k, num_experts, capacity, format,
                          tokens_per_expert, expert_offset, slot, src_token, recv_x, recv_scale, recv_weight,
@@ -254,7 +262,7 @@ EP_API ep_status ep_layout_dispatch_i64(const int64_t* topk_idx, const void* x, 
                                         int64_t num_tokens, int32_t hidden, int32_t top_k, int32_t num_experts,
                                         int32_t capacity, int32_t format, int32_t* tokens_per_expert,
                                         int32_t* expert_offset, int32_t* slot, int32_t* src_token, void* recv_x,
-                                        float* recv_scale, float* recv_weight, void* workspace,
+                                        void* recv_scale, float* recv_weight, void* workspace,
                                         size_t workspace_bytes, void* stream) {
   return layout_dispatch(topk_idx, x, topk_weights, num_tokens, hidden, top_k, num_experts, capacity, format,
                          tokens_per_expert, expert_offset, slot, src_token, recv_x, recv_scale, recv_weight,
@@ -304,7 +312,7 @@ EP_API ep_status ep_layout_dispatch_noalloc(const int32_t* topk_idx, const void*
                                             int64_t num_tokens, int32_t hidden, int32_t top_k, int32_t num_experts,
                                             int32_t capacity, int32_t format, int32_t* tokens_per_expert,
                                             int32_t* expert_offset, int32_t* slot, int32_t* src_token,
-                                            void* recv_x, float* recv_scale, float* recv_weight, void* stream) {
+                                            void* recv_x, void* recv_scale, float* recv_weight, void* stream) {
   ep_status st = check_layout_dispatch(topk_idx, x, topk_weights, num_tokens, hidden, top_k, num_experts, capacity,
                                        format, tokens_per_expert, expert_offset, slot, src_token, recv_x,
                                        recv_scale, recv_weight, kCheckOnly, SIZE_MAX);
@@ -371,7 +379,7 @@ struct Plan {
   int32_t* slot;
   int32_t* src;
   void* recv_x;
-  float* recv_scale;
+  void* recv_scale;
   float* recv_weight;
   void* workspace;
   const void* y;
@@ -386,7 +394,7 @@ ep_status plan_layout_dispatch(const Plan& p) {
   return from_hip(ep::launch_layout_dispatch(
       static_cast<const Idx*>(p.topk_idx), static_cast<const uint16_t*>(p.x), p.topk_weights,
       static_cast<int32_t>(p.num_tokens), p.hidden, p.top_k, p.num_experts, p.capacity,
-      p.format == EP_RECV_FP8_E4M3_G128, p.counts, p.capacity == 0 ? p.offsets : nullptr, p.slot, p.src, p.recv_x,
+      p.format, p.counts, p.capacity == 0 ? p.offsets : nullptr, p.slot, p.src, p.recv_x,
       p.recv_scale, p.recv_weight, p.workspace, static_cast<hipStream_t>(p.stream)));
 }
 
@@ -396,7 +404,7 @@ EP_API ep_status ep_step_plan_init(ep_step_plan* plan, const void* topk_idx, int
                                    const float* topk_weights, int64_t num_tokens, int32_t hidden, int32_t top_k,
                                    int32_t num_experts, int32_t capacity, int32_t format,
                                    int32_t* tokens_per_expert, int32_t* expert_offset, int32_t* slot,
-                                   int32_t* src_token, void* recv_x, float* recv_scale, float* recv_weight,
+                                   int32_t* src_token, void* recv_x, void* recv_scale, float* recv_weight,
                                    void* workspace, size_t workspace_bytes, const void* y, void* out,
                                    void* stream) {
   if (plan == nullptr || !aligned(plan, alignof(ep_step_plan))) return EP_ERR_INVALID_ARG;
@@ -473,6 +481,108 @@ EP_API ep_status ep_combine_backward(const void* grad_out, const void* y, const 
       static_cast<const uint16_t*>(grad_out), static_cast<const uint16_t*>(y), slot, topk_weights,
       static_cast<int32_t>(num_tokens), hidden, top_k, static_cast<uint16_t*>(grad_y), grad_w,
       static_cast<hipStream_t>(stream)));
+}
+
+// ---- routing, rows and the experts' products ---------------------------------
+
+namespace {
+
+ep_status check_route(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t K, int32_t score, float scale) {
+  if (E < 1 || K < 1) return EP_ERR_INVALID_ARG;
+  if (E > EP_MAX_EXPERTS) return EP_ERR_UNSUPPORTED;
+  const ep_status st = check_common(T, K);
+  if (st != EP_OK) return st;
+  if (K > E) return EP_ERR_INVALID_ARG;
+  if (dtype != EP_DTYPE_F32 && dtype != EP_DTYPE_BF16) return EP_ERR_INVALID_ARG;
+  if (score != EP_SCORE_SOFTMAX && score != EP_SCORE_SIGMOID) return EP_ERR_INVALID_ARG;
+  if (!(scale - scale == 0.0f)) return EP_ERR_INVALID_ARG;  // finite
+  if (T == 0) return EP_OK;
+  if (!logits || !aligned(logits, dtype == EP_DTYPE_BF16 ? 2 : 4)) return EP_ERR_INVALID_ARG;
+  return EP_OK;
+}
+
+// Quantised rows: codes, scales and the BF16 rows they come from or go to.
+ep_status check_rows(const void* x, int64_t rows, int32_t H, int32_t format, const void* q, const void* scale) {
+  if (rows < 0 || H <= 0) return EP_ERR_INVALID_ARG;
+  if (format != EP_RECV_FP8_E4M3_G128 && format != EP_RECV_MXFP4_G32) return EP_ERR_INVALID_ARG;
+  if (H % (format == EP_RECV_FP8_E4M3_G128 ? 128 : 32) != 0) return EP_ERR_INVALID_ARG;
+  if (rows >= kMaxElems / H + (kMaxElems % H != 0)) return EP_ERR_UNSUPPORTED;  // rows * H >= kMaxElems
+  if (rows == 0) return EP_OK;
+  if (!x || !q || !scale) return EP_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16)) return EP_ERR_INVALID_ARG;
+  if (format == EP_RECV_FP8_E4M3_G128 && !aligned(scale, 4)) return EP_ERR_INVALID_ARG;
+  return EP_OK;
+}
+
+}  // namespace
+
+EP_API ep_status ep_route(const void* logits, int32_t logits_dtype, const float* bias, int64_t num_tokens,
+                          int32_t num_experts, int32_t top_k, int32_t n_group, int32_t topk_group, int32_t score,
+                          int32_t renormalize, float scale, int32_t* topk_idx, float* topk_weights, void* stream) {
+  const ep_status st = check_route(logits, logits_dtype, num_tokens, num_experts, top_k, score, scale);
+  if (st != EP_OK) return st;
+  if (n_group < 1 || topk_group < 1 || topk_group > n_group || num_experts % n_group != 0) return EP_ERR_INVALID_ARG;
+  if (n_group > EP_MAX_GROUPS) return EP_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return EP_OK;
+  if (!topk_idx || !topk_weights || !aligned(topk_idx, 4) || !aligned(topk_weights, 4) || !aligned(bias, 4))
+    return EP_ERR_INVALID_ARG;
+  return from_hip(ep::launch_route(logits, logits_dtype == EP_DTYPE_BF16, bias, static_cast<int32_t>(num_tokens),
+                                   num_experts, top_k, n_group, topk_group, score, renormalize != 0, scale, topk_idx,
+                                   topk_weights, static_cast<hipStream_t>(stream)));
+}
+
+EP_API ep_status ep_route_backward(const float* grad_w, const void* logits, int32_t logits_dtype,
+                                   const int32_t* topk_idx, int64_t num_tokens, int32_t num_experts, int32_t top_k,
+                                   int32_t score, int32_t renormalize, float scale, void* grad_logits, void* stream) {
+  const ep_status st = check_route(logits, logits_dtype, num_tokens, num_experts, top_k, score, scale);
+  if (st != EP_OK) return st;
+  if (num_tokens == 0) return EP_OK;
+  if (!grad_w || !topk_idx || !grad_logits || !aligned(grad_w, 4) || !aligned(topk_idx, 4) ||
+      !aligned(grad_logits, logits_dtype == EP_DTYPE_BF16 ? 2 : 4))
+    return EP_ERR_INVALID_ARG;
+  return from_hip(ep::launch_route_backward(grad_w, logits, logits_dtype == EP_DTYPE_BF16, topk_idx,
+                                            static_cast<int32_t>(num_tokens), num_experts, top_k, score,
+                                            renormalize != 0, scale, grad_logits, static_cast<hipStream_t>(stream)));
+}
+
+EP_API ep_status ep_quantize_rows(const void* x, int64_t num_rows, int32_t hidden, int32_t format, void* q,
+                                  void* scale, void* stream) {
+  const ep_status st = check_rows(x, num_rows, hidden, format, q, scale);
+  if (st != EP_OK || num_rows == 0) return st;
+  return from_hip(ep::launch_quantize_rows(static_cast<const uint16_t*>(x), num_rows, hidden,
+                                           format == EP_RECV_FP8_E4M3_G128, q, scale,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+EP_API ep_status ep_dequantize_rows(const void* q, const void* scale, int64_t num_rows, int32_t hidden,
+                                    int32_t format, void* x, void* stream) {
+  const ep_status st = check_rows(x, num_rows, hidden, format, q, scale);
+  if (st != EP_OK || num_rows == 0) return st;
+  return from_hip(ep::launch_dequantize_rows(q, scale, num_rows, hidden, format == EP_RECV_FP8_E4M3_G128,
+                                             static_cast<uint16_t*>(x), static_cast<hipStream_t>(stream)));
+}
+
+EP_API ep_status ep_expert_product(const void* a, const void* a_scale, int32_t a_format, const void* w,
+                                   const void* w_scale, const int32_t* expert_rows, int64_t num_rows,
+                                   int32_t num_experts, int32_t capacity, int32_t hidden, int32_t out_channels,
+                                   int32_t activation, void* y, void* stream) {
+  if (a_format != EP_RECV_FP8_E4M3_G128 && a_format != EP_RECV_MXFP4_G32) return EP_ERR_INVALID_ARG;
+  if (activation != EP_ACT_NONE && activation != EP_ACT_SWIGLU) return EP_ERR_INVALID_ARG;
+  const bool gated = activation == EP_ACT_SWIGLU;
+  if (num_rows < 0 || num_experts < 1 || capacity < 0 || hidden <= 0 || out_channels <= 0) return EP_ERR_INVALID_ARG;
+  if (hidden % 128 != 0 || out_channels % (gated ? 16 : 8) != 0) return EP_ERR_INVALID_ARG;
+  if (num_experts > EP_MAX_EXPERTS || hidden > 65536 || out_channels > 65536) return EP_ERR_UNSUPPORTED;
+  if (num_rows >= (int64_t(1) << 31)) return EP_ERR_UNSUPPORTED;
+  if (num_rows * (hidden > out_channels ? hidden : out_channels) >= kMaxElems) return EP_ERR_UNSUPPORTED;
+  if (capacity > 0 && num_rows != static_cast<int64_t>(num_experts) * capacity) return EP_ERR_INVALID_ARG;
+  if (num_rows == 0) return EP_OK;
+  if (!a || !a_scale || !w || !w_scale || !expert_rows || !y) return EP_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(y, 16)) return EP_ERR_INVALID_ARG;
+  if (!aligned(a_scale, 4) || !aligned(w_scale, 4) || !aligned(expert_rows, 4)) return EP_ERR_INVALID_ARG;
+  return from_hip(ep::launch_expert_product(a, a_scale, a_format == EP_RECV_FP8_E4M3_G128, w, w_scale, expert_rows,
+                                            static_cast<int32_t>(num_rows), num_experts, capacity, hidden,
+                                            out_channels, gated, static_cast<uint16_t*>(y),
+                                            static_cast<hipStream_t>(stream)));
 }
 
 EP_API ep_status ep_cast_fp8_e4m3(const float* in, uint8_t* out, int64_t n, void* stream) {

@@ -51,6 +51,7 @@
 // empty launch of the same grid takes 1.7 us and one that only loads the
 // token and ids and stores the 7.3 MB of rows 2.9 us.
 
+#include "../../include/ep.h"
 #include "ep_device.h"
 #include "ep_internal.h"
 
@@ -346,18 +347,24 @@ void launch_fused_ns(const Idx* idx, const uint16_t* x, const float* w, int32_t 
 template <typename Idx>
 hipError_t launch_layout_dispatch(const Idx* topk_idx, const uint16_t* x, const float* topk_weights,
                                   int32_t num_tokens, int32_t hidden, int32_t top_k, int32_t num_experts,
-                                  int32_t capacity, bool fp8, int32_t* counts, int32_t* offsets, int32_t* slot,
-                                  int32_t* src, void* recv, float* recv_scale, float* recv_weight,
+                                  int32_t capacity, int32_t format, int32_t* counts, int32_t* offsets,
+                                  int32_t* slot, int32_t* src, void* recv, void* scale, float* recv_weight,
                                   void* workspace, hipStream_t stream) {
   const int64_t n = static_cast<int64_t>(num_tokens) * top_k;
-  if (n > kFusedMaxEntries) {
+  const bool fp8 = format == EP_RECV_FP8_E4M3_G128, mxfp4 = format == EP_RECV_MXFP4_G32;
+  float* recv_scale = static_cast<float*>(scale);
+  if (n > kFusedMaxEntries || mxfp4) {
     hipError_t e = hipSuccess;
-    if (launch_layout_dispatch_chunked(topk_idx, x, topk_weights, num_tokens, hidden, top_k, num_experts, capacity,
+    if (!mxfp4 &&
+        launch_layout_dispatch_chunked(topk_idx, x, topk_weights, num_tokens, hidden, top_k, num_experts, capacity,
                                        fp8, counts, offsets, slot, src, recv, recv_scale, recv_weight, stream, &e))
       return e;
     e = launch_layout(topk_idx, static_cast<int32_t>(n), top_k, num_experts, capacity, counts, offsets,
                                  slot, src, workspace, stream);
     if (e != hipSuccess) return e;
+    if (mxfp4)
+      return launch_dispatch_mxfp4(x, num_tokens, hidden, top_k, slot, topk_weights, static_cast<uint8_t*>(recv),
+                                   static_cast<uint8_t*>(scale), recv_weight, stream);
     return fp8 ? launch_dispatch_fp8(x, num_tokens, hidden, top_k, slot, topk_weights, static_cast<uint8_t*>(recv),
                                      recv_scale, recv_weight, stream)
                : launch_dispatch_bf16(x, num_tokens, hidden, top_k, slot, topk_weights,
@@ -373,10 +380,10 @@ hipError_t launch_layout_dispatch(const Idx* topk_idx, const uint16_t* x, const 
 }
 
 template hipError_t launch_layout_dispatch<int32_t>(const int32_t*, const uint16_t*, const float*, int32_t, int32_t,
-                                                    int32_t, int32_t, int32_t, bool, int32_t*, int32_t*, int32_t*,
-                                                    int32_t*, void*, float*, float*, void*, hipStream_t);
+                                                    int32_t, int32_t, int32_t, int32_t, int32_t*, int32_t*, int32_t*,
+                                                    int32_t*, void*, void*, float*, void*, hipStream_t);
 template hipError_t launch_layout_dispatch<int64_t>(const int64_t*, const uint16_t*, const float*, int32_t, int32_t,
-                                                    int32_t, int32_t, int32_t, bool, int32_t*, int32_t*, int32_t*,
-                                                    int32_t*, void*, float*, float*, void*, hipStream_t);
+                                                    int32_t, int32_t, int32_t, int32_t, int32_t*, int32_t*, int32_t*,
+                                                    int32_t*, void*, void*, float*, void*, hipStream_t);
 
 }  // namespace ep

@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from . import api
-from ._lib import EP_RECV_BF16, EP_RECV_FP8_E4M3_G128, LIB, STEP_PLAN_WORDS, check
+from ._lib import EP_RECV_FP8_E4M3_G128, EP_RECV_MXFP4_G32, LIB, STEP_PLAN_WORDS, check
 
 
 class StepPlan:
@@ -23,7 +23,7 @@ class StepPlan:
     topk_idx int32 or int64 [T, K]; topk_weights float32 [T, K]; x bf16 [T, H];
     capacity 0 for the packed layout (T*K receive rows) or the rows per
     expert of the low-latency layout (E*capacity rows); fp8 selects the
-    receive format.  y (expert outputs, bf16 [rows, H]) defaults to a new
+    receive format, or format (EP_RECV_*) where it is given.  y (expert outputs, bf16 [rows, H]) defaults to a new
     tensor; all other buffers are allocated here.  The stream is fixed at
     construction (the current stream by default).  To replay a step as a
     HIP graph, build the plan on a side stream and capture on it:
@@ -32,7 +32,8 @@ class StepPlan:
     on different streams may run at the same time.
     """
 
-    def __init__(self, topk_idx, topk_weights, x, num_experts, capacity=0, fp8=True, y=None, stream=None):
+    def __init__(self, topk_idx, topk_weights, x, num_experts, capacity=0, fp8=True, y=None, stream=None,
+                 format=None):
         api._need(topk_idx, "topk_idx", api._IDX)
         if topk_idx.dim() != 2:
             raise ValueError("topk_idx must be [T, K]")
@@ -43,8 +44,11 @@ class StepPlan:
             raise ValueError("x must be [T, H]")
         H = x.shape[1]
         E = int(num_experts)
-        if fp8 and H % 128:
+        self.fmt = api._format(fp8, format)
+        if self.fmt == EP_RECV_FP8_E4M3_G128 and H % 128:
             raise ValueError("FP8 dispatch needs hidden % 128 == 0")
+        if self.fmt == EP_RECV_MXFP4_G32 and H % 32:
+            raise ValueError("MXFP4 rows need hidden % 32 == 0")
         if int(capacity) < 0:
             raise ValueError("capacity must be >= 0")
         self.T, self.H, self.K, self.E, self.capacity = T, H, K, E, int(capacity)
@@ -58,13 +62,7 @@ class StepPlan:
         self.src = torch.empty(rows, dtype=torch.int32, device=dev)
         nb = api.ep_layout_workspace_bytes(T, K, E)
         self.workspace = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
-        self.fmt = EP_RECV_FP8_E4M3_G128 if fp8 else EP_RECV_BF16
-        if fp8:
-            self.recv_x = torch.empty((rows, H), dtype=torch.uint8, device=dev)
-            self.recv_scale = torch.empty((rows, H // 128), dtype=torch.float32, device=dev)
-        else:
-            self.recv_x = torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
-            self.recv_scale = None
+        self.recv_x, self.recv_scale = api._new_recv(self.fmt, rows, H, dev)
         self.y = y if y is not None else torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
         api._need(self.y, "y", (torch.bfloat16, torch.int16, torch.uint16), (rows, H))
         self.out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)

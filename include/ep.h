@@ -57,11 +57,25 @@ typedef enum {
    * [R, G]; requires H % 128 == 0. */
   EP_RECV_FP8_E4M3_G128 = 0,
   /* the token's BF16 bits copied unchanged [R, H]; requires H % 8 == 0. */
-  EP_RECV_BF16 = 1
+  EP_RECV_BF16 = 1,
+  /* MXFP4 (OCP microscaling formats v1.0): E2M1 codes [R, H/2], two per
+   * byte with the even channel in the low half, plus one E8M0 scale byte
+   * per 32 channels [R, H/32]; requires H % 32 == 0. */
+  EP_RECV_MXFP4_G32 = 2
 } ep_recv_format;
+
+typedef enum { EP_DTYPE_F32 = 0, EP_DTYPE_BF16 = 1 } ep_dtype;
+
+/* How ep_route turns logits into scores. */
+typedef enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 } ep_score;
+
+/* What ep_expert_product does with its sums. */
+typedef enum { EP_ACT_NONE = 0, EP_ACT_SWIGLU = 1 } ep_activation;
 
 #define EP_MAX_EXPERTS 1024
 #define EP_MAX_TOPK 32
+
+#define EP_MAX_GROUPS 64 /* expert groups of ep_route */
 
 /* Human-readable name of a status code (static storage). */
 const char* ep_status_string(int status);
@@ -161,23 +175,30 @@ ep_status ep_dispatch_layout_padded_i64(const int64_t* topk_idx, int64_t num_tok
  * and for each unmasked k with r = slot[t,k]:
  *   recv_x[r, :] = q,  recv_scale[r, g] = s,  recv_weight[r] = topk_weights[t,k].
  * With EP_RECV_BF16, recv_x[r, :] = x[t, :] bit for bit and recv_scale is
- * unused (may be NULL).
+ * unused (may be NULL).  With EP_RECV_MXFP4_G32, per group of 32 channels:
+ *   a = max |x[t,c]|,  e = max(floor(log2 a) - 2, -127)  (e = 0 if a == 0),
+ *   q[c] = E2M1_RNE(x[t,c] / 2^e), magnitudes beyond 6 saturating to 6,
+ *   recv_scale[r, g] = e + 127 as a byte;
+ * a group that holds an infinity or a NaN gets scale byte 255 (NaN) and
+ * zero codes.
  *
  * x            bf16 bits [T, H] in, 16-byte aligned
  * slot         int32 [T, K] from ep_dispatch_layout
  * topk_weights float32 [T, K] or NULL (then recv_weight must be NULL)
- * recv_x       [rows, H] out: uint8 (FP8) or bf16 bits, 16-byte aligned;
- *              rows = T*K for ep_dispatch_layout's slot, E*capacity for
+ * recv_x       [rows, H] out: uint8 (FP8) or bf16 bits, or [rows, H/2]
+ *              bytes (MXFP4), 16-byte aligned; rows = T*K for
+ *              ep_dispatch_layout's slot, E*capacity for
  *              ep_dispatch_layout_padded's
- * recv_scale   float32 [rows, G] out (FP8 only), 4-byte aligned
+ * recv_scale   float32 [rows, G] out, 4-byte aligned (FP8), or bytes
+ *              [rows, H/32] out (MXFP4)
  * recv_weight  float32 [rows] out or NULL
  * Rows no entry maps to are left untouched.  Requirements: H > 0,
- * H % 128 == 0 for FP8, H % 8 == 0 for BF16, 1 <= K <= EP_MAX_TOPK,
- * T*K <= 2^22, T*H < 2^34.
+ * H % 128 == 0 for FP8, H % 32 == 0 for MXFP4, H % 8 == 0 for BF16,
+ * 1 <= K <= EP_MAX_TOPK, T*K <= 2^22, T*H < 2^34.
  */
 ep_status ep_dispatch(const void* x, int64_t num_tokens, int32_t hidden, int32_t top_k,
                       const int32_t* slot, const float* topk_weights, int32_t format,
-                      void* recv_x, float* recv_scale, float* recv_weight, void* stream);
+                      void* recv_x, void* recv_scale, float* recv_weight, void* stream);
 
 /*
  * ep_layout_dispatch - layout and dispatch in one call, the shape of the
@@ -194,8 +215,8 @@ ep_status ep_dispatch(const void* x, int64_t num_tokens, int32_t hidden, int32_t
  * dispatches its own tokens (when its share fits: at most 8 FP8 or 14 BF16
  * work items per lane of 1024, at most one entry per lane, and the
  * layout's LDS within the 160 KB of a workgroup, e.g. 4096 tokens of hidden
- * 7168 at top-8; else as beyond); beyond, the same launches as the
- * separate calls.
+ * 7168 at top-8; else as beyond); beyond, and for MXFP4, the same launches
+ * as the separate calls.
  *
  * topk_idx, tokens_per_expert, slot, src_token, workspace: as for
  *   ep_dispatch_layout (capacity == 0) or ep_dispatch_layout_padded
@@ -210,7 +231,7 @@ ep_status ep_layout_dispatch(const int32_t* topk_idx, const void* x, const float
                              int64_t num_tokens, int32_t hidden, int32_t top_k, int32_t num_experts,
                              int32_t capacity, int32_t format, int32_t* tokens_per_expert,
                              int32_t* expert_offset, int32_t* slot, int32_t* src_token, void* recv_x,
-                             float* recv_scale, float* recv_weight, void* workspace,
+                             void* recv_scale, float* recv_weight, void* workspace,
                              size_t workspace_bytes, void* stream);
 
 /* ep_layout_dispatch with int64 expert ids (8-byte aligned); otherwise identical. */
@@ -218,7 +239,7 @@ ep_status ep_layout_dispatch_i64(const int64_t* topk_idx, const void* x, const f
                                  int64_t num_tokens, int32_t hidden, int32_t top_k, int32_t num_experts,
                                  int32_t capacity, int32_t format, int32_t* tokens_per_expert,
                                  int32_t* expert_offset, int32_t* slot, int32_t* src_token, void* recv_x,
-                                 float* recv_scale, float* recv_weight, void* workspace,
+                                 void* recv_scale, float* recv_weight, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
 /*
@@ -245,7 +266,7 @@ ep_status ep_layout_dispatch_noalloc(const int32_t* topk_idx, const void* x, con
                                      int64_t num_tokens, int32_t hidden, int32_t top_k, int32_t num_experts,
                                      int32_t capacity, int32_t format, int32_t* tokens_per_expert,
                                      int32_t* expert_offset, int32_t* slot, int32_t* src_token, void* recv_x,
-                                     float* recv_scale, float* recv_weight, void* stream);
+                                     void* recv_scale, float* recv_weight, void* stream);
 
 /*
  * ep_combine - reduce each token's K expert outputs back to the token.
@@ -311,7 +332,7 @@ ep_status ep_step_plan_init(ep_step_plan* plan, const void* topk_idx, int32_t id
                             const float* topk_weights, int64_t num_tokens, int32_t hidden, int32_t top_k,
                             int32_t num_experts, int32_t capacity, int32_t format, int32_t* tokens_per_expert,
                             int32_t* expert_offset, int32_t* slot, int32_t* src_token, void* recv_x,
-                            float* recv_scale, float* recv_weight, void* workspace, size_t workspace_bytes,
+                            void* recv_scale, float* recv_weight, void* workspace, size_t workspace_bytes,
                             const void* y, void* out, void* stream);
 
 /* The plan's ep_layout_dispatch launch. */
@@ -360,6 +381,115 @@ ep_status ep_dispatch_backward(const void* grad_recv, const int32_t* slot, int64
 ep_status ep_combine_backward(const void* grad_out, const void* y, const int32_t* slot,
                               const float* topk_weights, int64_t num_tokens, int32_t hidden, int32_t top_k,
                               void* grad_y, float* grad_w, void* stream);
+
+/*
+ * ep_route - from router scores to the ids and weights dispatch takes.
+ *
+ * [P1 "DeepEP 的常规内核和低延迟内核"] names the setting (top-4 groups,
+ * top-8 experts); the rule is not given by the pages and is, per token:
+ *   z = logits (NaN counts as -inf, +inf as the largest binary32); an
+ *       expert with z = -inf is switched off and never chosen
+ *   s = 1 / (1 + exp(-z))           EP_SCORE_SIGMOID
+ *   s = exp(z) / sum_e exp(z)       EP_SCORE_SOFTMAX
+ *   v = s + bias                    (bias steers the choice only)
+ *   with n_group > 1, group j holds experts j*E/n_group ..; its score is
+ *       the sum of its two largest v (of its only one), rounded to a
+ *       multiple of 2^-40; the topk_group best groups are kept
+ *   the K best experts of the kept groups are chosen, in descending order
+ *       of v (of z where there is no bias); ties go to the lower index
+ *   topk_idx[k] = the expert, topk_weights[k] = scale * s / S, where S is
+ *       the sum of the chosen s (renormalize) or 1.
+ * The choice is that of binary64 scores.  Weights are binary32, within
+ * 2^-20 of their value relatively.  Where fewer than K experts are left,
+ * the entries behind them get id -1 (masked everywhere in this library)
+ * and weight 0.
+ *
+ * logits       float32 or bf16 [T, E] (logits_dtype: ep_dtype), aligned to
+ *              an element
+ * bias         float32 [E] or NULL; -inf or NaN switches an expert off
+ * topk_idx     int32 [T, K] out;  topk_weights float32 [T, K] out
+ * Requirements: 1 <= E <= EP_MAX_EXPERTS, 1 <= K <= min(E, EP_MAX_TOPK),
+ * 1 <= topk_group <= n_group <= EP_MAX_GROUPS, E % n_group == 0, scale
+ * finite, T*K <= 2^22.
+ */
+ep_status ep_route(const void* logits, int32_t logits_dtype, const float* bias, int64_t num_tokens,
+                   int32_t num_experts, int32_t top_k, int32_t n_group, int32_t topk_group, int32_t score,
+                   int32_t renormalize, float scale, int32_t* topk_idx, float* topk_weights, void* stream);
+
+/*
+ * ep_route_backward - gradient of ep_route's weights w.r.t. the logits
+ * (the choice itself, and so the bias, has none).  With g = grad_w, c =
+ * scale, q_k = s_k / S (S as in ep_route, over the entries of topk_idx):
+ *   sigmoid, renormalized:  grad[e_k] += c q_k (1 - s_k) (g_k - sum_j g_j q_j)
+ *   sigmoid:                grad[e_k] += c g_k s_k (1 - s_k)
+ *   softmax, renormalized:  grad[e_k] += c q_k (g_k - sum_j g_j q_j)
+ *   softmax:                grad[e] = s_e (sum_{k: e_k = e} c g_k - sum_j c g_j s_{e_j})
+ * in binary32, every other element of grad_logits 0.  Entries whose id is
+ * outside [0, E) or names a switched-off expert (z = -inf) count for
+ * nothing, whatever their grad_w holds; an id may occur more than once.
+ *
+ * grad_w float32 [T, K]; logits, topk_idx, score, renormalize, scale as
+ * for ep_route; grad_logits [T, E] out, of the logits' type.
+ */
+ep_status ep_route_backward(const float* grad_w, const void* logits, int32_t logits_dtype, const int32_t* topk_idx,
+                            int64_t num_tokens, int32_t num_experts, int32_t top_k, int32_t score,
+                            int32_t renormalize, float scale, void* grad_logits, void* stream);
+
+/*
+ * ep_quantize_rows - rows to the codes and scales ep_dispatch would write
+ * for them, in their own order: an expert's activations between its two
+ * products, or weight matrices (num_experts * out_channels rows) when a
+ * model is loaded.
+ *
+ * x bf16 [rows, H], 16-byte aligned; format EP_RECV_FP8_E4M3_G128 or
+ * EP_RECV_MXFP4_G32; q and scale as ep_dispatch's recv_x and recv_scale.
+ * Requirements: H % 128 == 0 (FP8), H % 32 == 0 (MXFP4), rows*H < 2^34.
+ */
+ep_status ep_quantize_rows(const void* x, int64_t num_rows, int32_t hidden, int32_t format, void* q, void* scale,
+                           void* stream);
+
+/*
+ * ep_dequantize_rows - the values that codes and scales stand for:
+ * BF16_RNE(code * scale), exact for MXFP4 unless it leaves BF16's range;
+ * NaN where the code (E4M3) or the scale (byte 255 of MXFP4) is NaN.
+ * Same formats, alignment and requirements; x bf16 [rows, H] out.
+ */
+ep_status ep_dequantize_rows(const void* q, const void* scale, int64_t num_rows, int32_t hidden, int32_t format,
+                             void* x, void* stream);
+
+/*
+ * ep_expert_product - every expert's weight matrix times the rows the
+ * dispatch gave it ([P5 "典型工作流程"]: the expert GEMM between dispatch
+ * and combine):
+ *   p[r, n] = sum_h w[e(r), n, h] * a[r, h]
+ *   y[r, n] = BF16_RNE(p[r, n])                                EP_ACT_NONE
+ *   y[r, i] = BF16_RNE(silu(p[r, i]) * p[r, N/2 + i])          EP_ACT_SWIGLU
+ * silu(u) = u / (1 + exp(-u)).  Sums and activation are binary32; the
+ * products of two codes are exact.  FP8 rows are summed per 128 channels
+ * before their scale is applied.
+ *
+ * a, a_scale   rows as ep_dispatch or ep_quantize_rows leave them, format
+ *              EP_RECV_MXFP4_G32 or EP_RECV_FP8_E4M3_G128
+ * w, w_scale   MXFP4 codes [E, N, H/2] and scale bytes [E, N, H/32]
+ * expert_rows  capacity == 0: expert_offset int32 [E+1] of the packed
+ *              layout, rows expert_offset[e] .. expert_offset[e+1]-1 are
+ *              expert e's; capacity > 0: recv_expert_count int32 [E] of the
+ *              padded layout, rows e*capacity .. e*capacity +
+ *              recv_expert_count[e] - 1 are.  Values outside the buffer
+ *              (below 0, beyond num_rows or capacity) are clamped to it.
+ * num_rows     rows of a and y: E*capacity for the padded layout
+ * y            bf16 [num_rows, N] (N/2 with EP_ACT_SWIGLU) out; rows of no
+ *              expert are left untouched; must not overlap the inputs
+ * a and w 16-byte aligned, y 16-byte aligned, a_scale, w_scale and
+ * expert_rows 4-byte aligned.
+ * Requirements: 1 <= E <= EP_MAX_EXPERTS, H % 128 == 0, H <= 65536,
+ * N % 8 == 0 (N % 16 == 0 with EP_ACT_SWIGLU), N <= 65536, num_rows <
+ * 2^31, num_rows * max(H, N) < 2^34.
+ */
+ep_status ep_expert_product(const void* a, const void* a_scale, int32_t a_format, const void* w,
+                            const void* w_scale, const int32_t* expert_rows, int64_t num_rows, int32_t num_experts,
+                            int32_t capacity, int32_t hidden, int32_t out_channels, int32_t activation, void* y,
+                            void* stream);
 
 /*
  * ep_cast_fp8_e4m3 - the binary32 -> E4M3FN conversion ep_dispatch uses,
