@@ -121,18 +121,13 @@ __global__ __launch_bounds__(kThreads) void product_kernel(const uint8_t* __rest
 // Workgroup tile: BN weight rows (with GATED half gate, half up, of the same
 // BN/2 channels of y) times BM token rows, over all of H in stages of 256
 // channels.  A stage's codes go from global memory straight to LDS (16 bytes a
-// lane), into one of two buffers while the other one is multiplied.  LDS rows
-// are 128 bytes (FP8 rows 256) and hold their 16-byte pieces in the order
-// piece ^ (row & 7) (& 15), so that eight lanes reading one piece of eight
-// rows meet all banks.  Scales go along 16 bytes a row (512 channels) at a
-// time, every second stage.
+// lane), into one of two buffers while the other one is multiplied; the copies
+// run on over the end of a tile into the next one.  LDS rows are 128 bytes
+// (FP8 rows 256) and hold their 16-byte pieces permuted (piece ^
+// swizzle(row)), so that the 16 lanes served together meet different banks.
+// Scales are copied 32 bytes a row, for four stages.
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-__device__ __forceinline__ void wait_loads() {
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the copies to LDS count there
-}
-
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 typedef __attribute__((address_space(3))) void LdsVoid;
 
@@ -144,10 +139,31 @@ __device__ __forceinline__ Rsrc make_rsrc(const void* p, uint32_t bytes) {
 __device__ __forceinline__ void copy16(Rsrc src, uint8_t* dst, uint32_t lane_off, uint32_t off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (LdsVoid*)dst, 16, lane_off, off, 0, 0);
 }
+// The same, non-temporal.
+__device__ __forceinline__ void copy16_once(Rsrc src, uint8_t* dst, uint32_t lane_off, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (LdsVoid*)dst, 16, lane_off, off, 0, 2);
+}
+
+// Until this wave's copies have arrived and its LDS reads are done; then the
+// workgroup's barrier.
+__device__ __forceinline__ void wait_and_sync() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t swizzle8(uint32_t row) { return (row & 7) ^ ((row >> 3) & 1); }
+__device__ __forceinline__ uint32_t swizzle16(uint32_t row) { return row & 15; }
 
 __device__ __forceinline__ i32x8 widen(u32x4 lo) {
-  return i32x8{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]), static_cast<int>(lo[3]), 0, 0, 0, 0};
+  return i32x8{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]), static_cast<int>(lo[3]),
+               0, 0, 0, 0};
 }
+
+// An offset past the end of every operand (at most 2^31 bytes of one expert's
+// weights, 2^24 of a tile's rows): buffer loads from there give 0.
+constexpr uint32_t kNone = 0x80000000u;
 
 template <bool FP8, bool GATED, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN* kWave) void product_tiled(
@@ -155,20 +171,21 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tiled(
     const uint8_t* __restrict__ w_scale, const int32_t* __restrict__ expert_rows, int32_t num_rows, int32_t E,
     int32_t capacity, int32_t H, int32_t N, uint16_t* __restrict__ y) {
   constexpr int NW = WM * WN, kThr = NW * kWave;
-  constexpr int TM = BM / WM, TN = BN / WN;    // a wave's rows and weight rows
-  constexpr int FM = TM / 32, FN = TN / 32;
-  constexpr int AB = FP8 ? 256 : 128;          // bytes of a token row in a stage
-  constexpr int LW = BN / 8 / NW;              // copies per wave and stage: 8 weight rows each
-  constexpr int LA = BM * AB / 1024 / NW;      // (1024 / AB token rows each)
+  constexpr int TN = BN / WN;                       // a wave's weight rows
+  constexpr int FM = BM / WM / 32, FN = TN / 32;    // its fragments of 32 rows
+  constexpr int AB = FP8 ? 256 : 128;               // bytes of a token row in a stage
+  constexpr int LW = BN / 8 / NW;                   // copies per wave and stage: 8 weight rows each
+  constexpr int LA = BM * AB / 1024 / NW;           // 1024 / AB token rows each
   static_assert(LW * 8 * NW == BN && LA * 1024 * NW == BM * AB && FM * 32 * WM == BM && FN * 32 * WN == BN, "tile");
   static_assert(!GATED || FN % 2 == 0, "a wave holds both halves of its channels");
-  constexpr int SR = BN + (BM < 64 ? 64 : BM);  // rows of scales, in copies of 64
-  constexpr int LS = (SR / 64 + NW - 1) / NW;   // those per wave
+  constexpr int SR = BN + BM;                       // rows of scales, in copies of 32
+  constexpr int LS = (SR / 32 + NW - 1) / NW;       // those per wave
+  constexpr int BO = GATED ? BN / 2 : BN;           // channels of y per tile
   __shared__ __align__(16) uint8_t w0[BN * 128];
   __shared__ __align__(16) uint8_t w1[BN * 128];
   __shared__ __align__(16) uint8_t a0[BM * AB];
   __shared__ __align__(16) uint8_t a1[BM * AB];
-  __shared__ __align__(16) uint8_t sc[2][SR * 16 + 16];
+  __shared__ __align__(16) uint8_t sc[SR * 32 + 16];
   __shared__ int start[kMaxExperts + 1];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -183,238 +200,275 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tiled(
   __syncthreads();
   block_exclusive_scan(start, E + 1);
   const int O = GATED ? N / 2 : N;
-  constexpr int BO = GATED ? BN / 2 : BN;  // channels of y per tile
-  const int nt = (O + BO - 1) / BO;
+  const uint32_t nt = (O + BO - 1) / BO;
   const uint32_t wrow_bytes = H / 2, arow_bytes = FP8 ? H : H / 2, srow_bytes = H / 32;
-  const int stages = (H + 255) / 256;
+  const int stages = (H + 255) / 256, quads = (stages + 3) / 4;
   const bool tail = (H & 255) != 0;  // the last stage holds 128 channels
   const uint32_t tiles = static_cast<uint32_t>(start[E]) * nt;
 
-  // tiles in eight runs, one per XCD (workgroups go to the XCDs in turn)
+  // Tiles in eight runs, one per XCD (workgroups go to the XCDs in turn), so
+  // that neighbouring tiles, which share weights or rows, meet in one L2.
   const uint32_t run = (tiles + 7) / 8, step = gridDim.x / 8;
-  for (uint32_t t = blockIdx.x / 8; t < run; t += step) {
-    const uint32_t tile = (blockIdx.x & 7) * run + t;
-    if (tile >= tiles) break;
+  uint32_t t = blockIdx.x / 8;
+  const uint32_t base = (blockIdx.x & 7) * run;
+  if (t >= run || base + t >= tiles) return;
+
+  // The tile whose stages are being copied: its operands and this lane's
+  // pieces.  Rows past the end repeat the last one.
+  int walk = 0, n0, rows, row0;
+  bool once;  // the expert's only row tile: its weights are read here alone
+  Rsrc wr, ar, wsr, asr;
+  uint32_t woff[LW], aoff[LA], soff[LS];
+  const auto open_tile = [&]() {
+    const uint32_t tile = base + t;
     const int q = static_cast<int>(tile / nt);
-    int lo = 0, hi = E;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (start[mid] <= q) lo = mid; else hi = mid;
-    }
-    const int e = __builtin_amdgcn_readfirstlane(lo);
+    while (__builtin_amdgcn_readfirstlane(start[walk + 1]) <= q) ++walk;  // q < start[E]
     int first, count;
-    rows_of(expert_rows, e, capacity, num_rows, first, count);
-    const uint32_t before = start[e], te = start[e + 1] - before;
+    rows_of(expert_rows, walk, capacity, num_rows, first, count);
+    const uint32_t before = __builtin_amdgcn_readfirstlane(start[walk]);
+    const uint32_t te = __builtin_amdgcn_readfirstlane(start[walk + 1]) - before;
     const uint32_t local = tile - before * nt;
-    const int m0 = __builtin_amdgcn_readfirstlane(static_cast<int>(local % te) * BM);
-    const int n0 = __builtin_amdgcn_readfirstlane(static_cast<int>(local / te) * BO);
-    first = __builtin_amdgcn_readfirstlane(first);
-    const int rows = __builtin_amdgcn_readfirstlane(min(count - m0, BM));  // >= 1
-    const size_t row0 = static_cast<size_t>(first) + m0;
-
-    const Rsrc wr = make_rsrc(w + static_cast<size_t>(e) * N * wrow_bytes, static_cast<uint32_t>(N) * wrow_bytes);
-    const Rsrc ar = make_rsrc(a + row0 * arow_bytes, static_cast<uint32_t>(rows) * arow_bytes);
-    const Rsrc wsr = make_rsrc(w_scale + static_cast<size_t>(e) * N * srow_bytes, static_cast<uint32_t>(N) * srow_bytes);
-    const Rsrc asr = make_rsrc(a_scale + row0 * srow_bytes, static_cast<uint32_t>(rows) * srow_bytes);
-
-    // this lane's pieces: rows past the end repeat the last one
-    const auto weight_row = [&](int r) -> uint32_t {
-      if (!GATED) return min(n0 + r, O - 1);
-      return r < BO ? min(n0 + r, O - 1) : O + min(n0 + r - BO, O - 1);
+    const int m0 = static_cast<int>(local % te) * BM;
+    once = te == 1;
+    n0 = static_cast<int>(local / te) * BO;
+    rows = __builtin_amdgcn_readfirstlane(min(count - m0, BM));  // >= 1
+    row0 = __builtin_amdgcn_readfirstlane(first) + m0;
+    const size_t we = static_cast<size_t>(walk) * N;
+    wr = make_rsrc(w + we * wrow_bytes, static_cast<uint32_t>(N) * wrow_bytes);
+    ar = make_rsrc(a + static_cast<size_t>(row0) * arow_bytes, static_cast<uint32_t>(rows) * arow_bytes);
+    wsr = make_rsrc(w_scale + we * srow_bytes, static_cast<uint32_t>(N) * srow_bytes);
+    asr = make_rsrc(a_scale + static_cast<size_t>(row0) * srow_bytes, static_cast<uint32_t>(rows) * srow_bytes);
+    const auto weight_row = [&](int r0, int r) -> uint32_t {  // r0: wave-uniform, of the same half as r
+      const uint32_t n = min(n0 + (GATED && r0 >= BO ? r - BO : r), O - 1);
+      return GATED && r0 >= BO ? n + O : n;
     };
-    uint32_t woff[LW], aoff[LA], soff[LS];
-    const uint32_t wpiece = (lane & 7) ^ (lane >> 3);
-    const uint32_t wcut = tail ? (wpiece & 4) * 16 : 0;  // in a last stage of 128 channels, stay inside the row
 #pragma unroll
-    for (int i = 0; i < LW; ++i) woff[i] = weight_row((wave * LW + i) * 8 + (lane >> 3)) * wrow_bytes + wpiece * 16;
-    uint32_t apiece, acut;
+    for (int i = 0; i < LW; ++i) {
+      const int r0 = (i * NW + wave) * 8, r = r0 + (lane >> 3);
+      woff[i] = weight_row(r0, r) * wrow_bytes + ((lane & 7) ^ swizzle8(r)) * 16;
+    }
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
-      constexpr int per = 1024 / AB;
-      const int r = (wave * LA + i) * per + lane / (AB / 16);
-      apiece = (lane % (AB / 16)) ^ (r & (AB / 16 - 1));
-      aoff[i] = min(r, rows - 1) * arow_bytes + apiece * 16;
+      const int r = (i * NW + wave) * (1024 / AB) + lane / (AB / 16);
+      aoff[i] = min(r, rows - 1) * arow_bytes + (FP8 ? (lane & 15) ^ swizzle16(r) : (lane & 7) ^ swizzle8(r)) * 16;
     }
-    // FP8: the piece depends on the copy (4 rows each); cut per copy below
-    acut = tail ? (AB == 128 ? (wpiece & 4) * 16 : 0) : 0;
 #pragma unroll
     for (int i = 0; i < LS; ++i) {
-      const int c = wave + i * NW;  // copy c: 64 rows of scales
-      soff[i] = (c < BN / 64 ? weight_row(c * 64 + lane) : min((c - BN / 64) * 64 + lane, rows - 1)) * srow_bytes;
+      const int r0 = (i * NW + wave) * 32, r = r0 + (lane >> 1);
+      soff[i] = (r0 < BN ? weight_row(r0, r) : min(r - BN, rows - 1)) * srow_bytes;
     }
+  };
+  // Part Q of 4 of a stage's copies.  In a last stage of 128 channels the
+  // pieces of the missing half are read past the end of the buffer resource
+  // (kNone), which gives zero codes.
+  const auto copy_part = [&](auto qc, int s, uint8_t* wb, uint8_t* ab) {
+    constexpr int Q = decltype(qc)::value;
+    const bool cut = tail && s == stages - 1;
+#pragma unroll
+    for (int i = Q; i < LW; i += 4) {
+      const int r0 = (i * NW + wave) * 8;
+      uint32_t off = woff[i];
+      if (cut && (((lane & 7) ^ swizzle8(r0 + (lane >> 3))) & 4)) off = kNone;
+      if (once) copy16_once(wr, wb + r0 * 128, off, s * 128); else copy16(wr, wb + r0 * 128, off, s * 128);
+    }
+#pragma unroll
+    for (int i = Q; i < LA; i += 4) {
+      const int r0 = (i * NW + wave) * (1024 / AB), r = r0 + lane / (AB / 16);
+      uint32_t off = aoff[i];
+      if (cut && (FP8 ? ((lane & 15) ^ swizzle16(r)) & 8 : ((lane & 7) ^ swizzle8(r)) & 4)) off = kNone;
+      if (r0 < rows) copy16(ar, ab + r0 * AB, off, s * AB);
+    }
+  };
+  const auto copy_stage = [&](int s, uint8_t* wb, uint8_t* ab) {
+    static_for<0, 4>([&](auto q) { copy_part(q, s, wb, ab); });
+  };
+  // 16 bytes of scales from 512-channel group g on, or the row's last 16
+  const auto scale_at = [&](uint32_t g) { return min(g * 16, srow_bytes - 16); };
+  const auto copy_scales = [&](int quad) {
+    const uint32_t at = scale_at(quad * 2 + (lane & 1));
+#pragma unroll
+    for (int i = 0; i < LS; ++i) {
+      const int r0 = (i * NW + wave) * 32;
+      if (r0 < BN) copy16(wsr, sc + r0 * 32, soff[i] + at, 0);
+      else if (r0 < BN + rows) copy16(asr, sc + r0 * 32, soff[i] + at, 0);
+    }
+  };
 
-    const auto copy_stage = [&](int st, uint8_t* wb, uint8_t* ab) {
-      const bool cut = tail && st == stages - 1;
+  // the wave's fragment i of weight rows, and j of token rows, in the tile
+  const auto weight_frag = [&](int i) {
+    if (!GATED) return wn * TN + i * 32;
+    return i < FN / 2 ? wn * (TN / 2) + i * 32 : BO + wn * (TN / 2) + (i - FN / 2) * 32;
+  };
+  const auto row_frag = [&](int j) { return (j * WM + wm) * 32; };  // in turn, so that short tiles keep all waves busy
+
+  f32x16 acc[FN][FM];
+  uint32_t sw[FN][4], sa[FM][4];  // scales of a pair of stages: one 32-bit word per 128 channels
+  const auto read_scales = [&](int pair) {
+    const auto read4 = [&](int r, uint32_t one, uint32_t(&v)[4]) {
+      if (pair * 4 + 4 <= H / 128) {
+        const u32x4 q = *reinterpret_cast<const u32x4*>(sc + ((pair & 1) * 16 + r * 32));
 #pragma unroll
-      for (int i = 0; i < LW; ++i)
-        copy16(wr, wb + (wave * LW + i) * 1024, woff[i] - (cut ? wcut : 0), st * 128);
+        for (int x = 0; x < 4; ++x) v[x] = q[x];
+      } else {
+        // the row's last 16 bytes were copied: the missing words, for zero
+        // codes, are a scale of 1
+        const uint32_t off = pair * 16 - scale_at(pair);
 #pragma unroll
-      for (int i = 0; i < LA; ++i) {
-        uint32_t c = acut;
-        if (AB == 256) {
-          const int r = (wave * LA + i) * 4 + lane / 16;
-          c = (((lane % 16) ^ (r & 15)) & 8) * 16;
+        for (int x = 0; x < 4; ++x)
+          v[x] = pair * 4 + x < H / 128
+                     ? *reinterpret_cast<const uint32_t*>(sc + ((pair & 1) * 16 + off + r * 32 + x * 4)) : one;
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      read4(weight_frag(i) + col, 0x7F7F7F7Fu, sw[i]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sw[i][x] >>= 8 * half;
+    }
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      read4(BN + row_frag(j) + col, FP8 ? 0x3F800000u : 0x7F7F7F7Fu, sa[j]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sa[j][x] >>= FP8 ? 0 : 8 * half;
+    }
+  };
+
+  const auto weight_piece = [&](int ks, int i, const uint8_t* wb) {
+    return widen(*reinterpret_cast<const u32x4*>(
+        wb + ((weight_frag(i) + col) * 128 + (((ks * 2 + half) ^ swizzle8(col)) * 16))));
+  };
+  const auto token_piece = [&](int ks, int j, const uint8_t* ab) {
+    const uint32_t r = row_frag(j) + col;
+    if constexpr (FP8) {
+      // this half-wave's 32 channels of a 64-channel step: 16 of each 32
+      const uint32_t p = ks * 4 + half;
+      const u32x4 lo4 = *reinterpret_cast<const u32x4*>(ab + (r * 256 + ((p ^ swizzle16(col)) * 16)));
+      const u32x4 hi4 = *reinterpret_cast<const u32x4*>(ab + (r * 256 + (((p + 2) ^ swizzle16(col)) * 16)));
+      return i32x8{static_cast<int>(lo4[0]), static_cast<int>(lo4[1]), static_cast<int>(lo4[2]), static_cast<int>(lo4[3]),
+                   static_cast<int>(hi4[0]), static_cast<int>(hi4[1]), static_cast<int>(hi4[2]), static_cast<int>(hi4[3])};
+    } else {
+      return widen(*reinterpret_cast<const u32x4*>(ab + (r * 128 + (((ks * 2 + half) ^ swizzle8(col)) * 16))));
+    }
+  };
+  // A stage's products: four steps of 64 channels times FM row fragments, in
+  // an order that keeps an FP8 fragment's two steps of one scale together;
+  // each is read two places ahead of its use.
+  constexpr int U = 4 * FM;
+  const auto step_of = [](int u) { return FP8 ? u / (2 * FM) * 2 + u % 2 : u / FM; };
+  const auto frag_of = [](int u) { return FP8 ? u / 2 % FM : u % FM; };
+  const auto multiply = [&](auto xc, const uint8_t* wb, const uint8_t* ab, auto&& copies) {
+    constexpr int X = decltype(xc)::value;  // first word of the stage's scales
+    i32x8 wv[4][FN], av[U];
+#pragma unroll
+    for (int i = 0; i < FN; ++i) wv[0][i] = weight_piece(0, i, wb);
+    av[0] = token_piece(0, 0, ab);
+    if constexpr (FP8) {
+#pragma unroll
+      for (int i = 0; i < FN; ++i) wv[1][i] = weight_piece(1, i, wb);
+    }
+    av[1] = token_piece(step_of(1), frag_of(1), ab);
+    f32x16 d[FN];
+    static_for<0, U>([&](auto uc) {
+      constexpr int u = decltype(uc)::value;
+      constexpr int ks = step_of(u), j = frag_of(u);
+      if constexpr (u + 2 < U) {
+        av[u + 2] = token_piece(step_of(u + 2), frag_of(u + 2), ab);
+      }
+      // the next step's weights (FP8: the next two steps')
+      if constexpr (!FP8 && u % FM == 0 && ks < 3) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i) wv[ks + 1][i] = weight_piece(ks + 1, i, wb);
+      }
+      if constexpr (FP8 && u == FM) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+          wv[2][i] = weight_piece(2, i, wb);
+          wv[3][i] = weight_piece(3, i, wb);
         }
-        copy16(ar, ab + (wave * LA + i) * 1024, aoff[i] - (cut ? c : 0), st * AB);
       }
-    };
-    const auto scale_at = [&](int pair) { return min(static_cast<uint32_t>(pair) * 16, srow_bytes - 16); };
-    const auto copy_scales = [&](int pair) {
+      if constexpr (u < 4 && u < U / 2) copies(uc);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < LS; ++i) {
-        const int c = wave + i * NW;
-        uint8_t* dst = sc[pair & 1] + c * 1024;
-        if (c < BN / 64) copy16(wsr, dst, soff[i], scale_at(pair));
-        else if (c < SR / 64) copy16(asr, dst, soff[i], scale_at(pair));
+      for (int i = 0; i < FN; ++i) {
+        const int s = static_cast<int>(sw[i][X + ks / 2]);
+        constexpr int sel = ks % 2 * 2;
+        if constexpr (FP8) {
+          if (ks % 2 == 0) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) d[i][r] = 0.0f;
+          }
+          d[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv[ks][i], av[u], d[i], kFp4, kFp8, sel, s, 0, 127);
+          if (ks % 2 == 1) {
+            const float f = __uint_as_float(sa[j][X + ks / 2]);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(f, d[i][r], acc[i][j][r]);
+          }
+        } else {
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv[ks][i], av[u], acc[i][j], kFp4, kFp4, sel, s, sel,
+                                                                     static_cast<int>(sa[j][X + ks / 2]));
+        }
       }
-    };
+    });
+  };
 
-    f32x16 acc[FN][FM];
+  open_tile();
+  copy_scales(0);
+  copy_stage(0, w0, a0);
+  for (;;) {
+    const int c_n0 = n0, c_rows = rows, c_row0 = row0;  // the tile being multiplied
+    bool last = false;
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
       for (int j = 0; j < FM; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-
-    // the wave's frag i of weight rows starts at this row of the tile
-    const auto frag_row = [&](int i) {
-      if (!GATED) return wn * TN + i * 32;
-      return i < FN / 2 ? wn * (TN / 2) + i * 32 : BO + wn * (TN / 2) + (i - FN / 2) * 32;
-    };
-
-    const auto multiply = [&](int st, const uint8_t* wb, const uint8_t* ab, const uint2 (&sw)[FN], const uint2 (&sa)[FM]) {
-      const int ksteps = tail && st == stages - 1 ? 2 : 4;
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        if (ks >= ksteps) break;
-        i32x8 av[FM], wv[FN];
-#pragma unroll
-        for (int i = 0; i < FN; ++i) {
-          const int r = frag_row(i) + col;
-          wv[i] = widen(*reinterpret_cast<const u32x4*>(wb + r * 128 + (((ks * 2 + half) ^ (r & 7)) * 16)));
+    const bool mine = wm * 32 < c_rows;  // else this wave's rows are all past the end
+    // stage 4 * quad + X, in (wb, ab); the next one goes to (wnext, anext)
+    const auto stage = [&](int quad, auto xc, const uint8_t* wb, const uint8_t* ab, uint8_t* wnext, uint8_t* anext) {
+      constexpr int X = decltype(xc)::value;
+      const int st = quad * 4 + X;
+      int to = st + 1;  // the stage to copy
+      wait_and_sync();
+      if (X % 2 == 0) read_scales(quad * 2 + X / 2);
+      if (X == 3) {
+        // the next quad's scales, or the next tile's first
+        const bool end = quad + 1 == quads;
+        if (end) {
+          t += step;
+          last = t >= run || base + t >= tiles;
+          if (!last) open_tile();
+          to = last ? stages : 0;
         }
-#pragma unroll
-        for (int j = 0; j < FM; ++j) {
-          const int r = wm * TM + j * 32 + col;
-          if constexpr (FP8) {
-            const u32x4 lo4 = *reinterpret_cast<const u32x4*>(ab + r * 256 + (((ks * 4 + half) ^ (r & 15)) * 16));
-            const u32x4 hi4 = *reinterpret_cast<const u32x4*>(ab + r * 256 + (((ks * 4 + 2 + half) ^ (r & 15)) * 16));
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              av[j][x] = static_cast<int>(lo4[x]);
-              av[j][4 + x] = static_cast<int>(hi4[x]);
-            }
-          } else {
-            av[j] = widen(*reinterpret_cast<const u32x4*>(ab + r * 128 + (((ks * 2 + half) ^ (r & 7)) * 16)));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < FN; ++i)
-#pragma unroll
-          for (int j = 0; j < FM; ++j) {
-            const int sx = ks < 2 ? sw[i].x : sw[i].y;
-            if constexpr (FP8) {
-              // handled per 128 channels in multiply_fp8
-            } else {
-              const int sy = ks < 2 ? sa[j].x : sa[j].y;
-              if (ks % 2 == 0)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv[i], av[j], acc[i][j], kFp4, kFp4, 0, sx, 0, sy);
-              else
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv[i], av[j], acc[i][j], kFp4, kFp4, 2, sx, 2, sy);
-            }
-          }
+        if (!last) copy_scales(end ? 0 : quad + 1);
+      }
+      const auto copies = [&](auto q) {
+        if (to < stages) copy_part(q, to, wnext, anext);
+      };
+      if (mine && st < stages) {
+        multiply(std::integral_constant<int, X % 2 * 2>{}, wb, ab, copies);
+        static_for<(U / 2 < 4 ? U / 2 : 4), 4>(copies);
+      } else {
+        static_for<0, 4>(copies);
       }
     };
-    const auto multiply_fp8 = [&](int st, const uint8_t* wb, const uint8_t* ab, const uint2 (&sw)[FN], const uint2 (&sa)[FM]) {
-      const int groups = tail && st == stages - 1 ? 1 : 2;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (g >= groups) break;
-        i32x8 av[2][FM], wv[2][FN];
-#pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
-          const int ks = g * 2 + k2;
-#pragma unroll
-          for (int i = 0; i < FN; ++i) {
-            const int r = frag_row(i) + col;
-            wv[k2][i] = widen(*reinterpret_cast<const u32x4*>(wb + r * 128 + (((ks * 2 + half) ^ (r & 7)) * 16)));
-          }
-#pragma unroll
-          for (int j = 0; j < FM; ++j) {
-            const int r = wm * TM + j * 32 + col;
-            const u32x4 lo4 = *reinterpret_cast<const u32x4*>(ab + r * 256 + (((ks * 4 + half) ^ (r & 15)) * 16));
-            const u32x4 hi4 = *reinterpret_cast<const u32x4*>(ab + r * 256 + (((ks * 4 + 2 + half) ^ (r & 15)) * 16));
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              av[k2][j][x] = static_cast<int>(lo4[x]);
-              av[k2][j][4 + x] = static_cast<int>(hi4[x]);
-            }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < FN; ++i)
-#pragma unroll
-          for (int j = 0; j < FM; ++j) {
-            const int sx = g == 0 ? sw[i].x : sw[i].y;
-            const float s = __uint_as_float(g == 0 ? sa[j].x : sa[j].y);
-            f32x16 d;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) d[r] = 0.0f;
-            d = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv[0][i], av[0][j], d, kFp4, kFp8, 0, sx, 0, 127);
-            d = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv[1][i], av[1][j], d, kFp4, kFp8, 2, sx, 0, 127);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(s, d[r], acc[i][j][r]);
-          }
-      }
-    };
-
-    // one stage: read its scales, start the next stage's copies, multiply
-    const auto stage = [&](int st, uint8_t* wb, uint8_t* ab, uint8_t* wnext, uint8_t* anext) {
-      uint2 sw[FN], sa[FM];
-      const int pair = st >> 1;
-      const uint32_t at = static_cast<uint32_t>(pair) * 16 - scale_at(pair) + (st & 1) * 8;
-      const uint8_t* sb = sc[pair & 1] + at;
-#pragma unroll
-      for (int i = 0; i < FN; ++i) {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(sb + (frag_row(i) + col) * 16);
-        sw[i] = uint2{p[0] >> (8 * half), p[1] >> (8 * half)};
-      }
-#pragma unroll
-      for (int j = 0; j < FM; ++j) {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(sb + (BN + wm * TM + j * 32 + col) * 16);
-        sa[j] = FP8 ? uint2{p[0], p[1]} : uint2{p[0] >> (8 * half), p[1] >> (8 * half)};
-      }
-      if (st + 1 < stages) {
-        if ((st & 1) == 0 && st + 2 < stages) copy_scales(pair + 1);
-        copy_stage(st + 1, wnext, anext);
-      }
-      if (wm * TM < rows) {  // else this wave's rows are all past the end
-        if constexpr (FP8) multiply_fp8(st, wb, ab, sw, sa); else multiply(st, wb, ab, sw, sa);
-      }
-      wait_loads();
-      __syncthreads();
-    };
-
-    copy_scales(0);
-    copy_stage(0, w0, a0);
-    wait_loads();
-    __syncthreads();
-    for (int st = 0; st < stages; st += 2) {
-      stage(st, w0, a0, w1, a1);
-      if (st + 1 < stages) stage(st + 1, w1, a1, w0, a0);
+    for (int quad = 0; quad < quads; ++quad) {
+      stage(quad, std::integral_constant<int, 0>{}, w0, a0, w1, a1);
+      stage(quad, std::integral_constant<int, 1>{}, w1, a1, w0, a0);
+      stage(quad, std::integral_constant<int, 2>{}, w0, a0, w1, a1);
+      stage(quad, std::integral_constant<int, 3>{}, w1, a1, w0, a0);
     }
 
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
-      const int m = wm * TM + j * 32 + col;
-      if (m >= rows) continue;
-      uint16_t* yrow = y + (row0 + m) * O;
+      const int m = row_frag(j) + col;
+      if (m >= c_rows) continue;
+      uint16_t* yrow = y + static_cast<size_t>(c_row0 + m) * O;
 #pragma unroll
       for (int i = 0; i < (GATED ? FN / 2 : FN); ++i)
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
-          const int n = n0 + frag_row(i) + 8 * r4 + 4 * half;
+          const int n = c_n0 + weight_frag(i) + 8 * r4 + 4 * half;
           if (n >= O) continue;
           __bf16 o[4];
 #pragma unroll
@@ -425,6 +479,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tiled(
           *reinterpret_cast<uint2*>(yrow + n) = *reinterpret_cast<uint2*>(o);
         }
     }
+    if (last) break;
   }
 }
 
@@ -444,13 +499,18 @@ hipError_t launch_expert_product(const void* a, const void* a_scale, bool fp8, c
   };
   const auto pick = [&](auto f, auto g) {
     constexpr bool F = decltype(f)::value, G = decltype(g)::value;
+    // rows too short for 16-byte pieces of scales
     if (H < 512) return with(product_kernel<F, G>, 2048, kThreads);
-    const int64_t avg = num_rows / E;
-    if (avg <= 48 || capacity > 0) return with(product_tiled<F, G, 32, 128, 1, 2>, 768, 128);
-    if constexpr (!F) {
-      if (avg > 192) return with(product_tiled<F, G, 256, 256, 2, 4>, 256, 512);
+    const int64_t avg = capacity > 0 ? 0 : num_rows / E;
+    if constexpr (F) {
+      if (avg <= 16) return with(product_tiled<F, G, 64, 128, 2, 2>, 512, 256);
+      return with(product_tiled<F, G, 128, 256, 2, 4>, 256, 512);
+    } else {
+      if (avg <= 16) return with(product_tiled<F, G, 32, 128, 1, 2>, 768, 128);
+      if (avg <= 64) return with(product_tiled<F, G, 128, 128, 2, 2>, 512, 256);
+      if (avg <= 170) return with(product_tiled<F, G, 192, 256, 2, 4>, 256, 512);
+      return with(product_tiled<F, G, 256, 256, 2, 4>, 256, 512);
     }
-    return with(product_tiled<F, G, 128, 256, 2, 4>, 256, 512);
   };
   if (fp8) return gated ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{});
   return gated ? pick(std::false_type{}, std::true_type{}) : pick(std::false_type{}, std::false_type{});
