@@ -11,6 +11,7 @@ and a handle, and ``combine(...)`` reducing back ([P4] "使用示例 › MoE 训
 的应用"; [P5] "典型工作流程").
 """
 
+import contextlib
 import os
 from collections import namedtuple
 
@@ -24,8 +25,13 @@ Handle = namedtuple("Handle", "tokens_per_expert expert_offset slot src_token nu
 PaddedHandle = namedtuple("PaddedHandle", "recv_expert_count slot src_token num_experts capacity")
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object: a few us less per call
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -106,12 +112,17 @@ def _format(fp8, format):
     return EP_RECV_FP8_E4M3_G128 if fp8 else EP_RECV_BF16
 
 
-def _same_device(first, *others):
-    """The operands' one device; launches go to that device's current stream."""
+_here = contextlib.nullcontext()
+
+
+def _device_of(first, *others):
+    """A context with the operands' one device current: launches go to that
+    device, and to its current stream."""
+    i = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != i:
             raise ValueError("operands on different devices: %s and %s" % (first.device, t.device))
-    return first.device
+    return _here if i == torch.cuda.current_device() else torch.cuda.device(i)
 
 
 def _ids_fn(name, topk_idx):
@@ -371,7 +382,7 @@ def ep_route(logits, bias, n_group, topk_group, score, renormalize, scale, topk_
         raise ValueError("topk_idx must be [T, K]")
     K = topk_idx.shape[1]
     _need(topk_weights, "topk_weights", _F32, (T, K))
-    with torch.cuda.device(_same_device(logits, bias, topk_idx, topk_weights)):
+    with _device_of(logits, bias, topk_idx, topk_weights):
         check("ep_route", LIB.ep_route(
             logits.data_ptr(), _logits_dtype(logits), bias.data_ptr() if bias is not None else None, T, E, K,
             int(n_group), int(topk_group), int(score), int(bool(renormalize)), float(scale), topk_idx.data_ptr(),
@@ -392,7 +403,7 @@ def ep_route_backward(grad_w, logits, topk_idx, score, renormalize, scale, grad_
     K = topk_idx.shape[1]
     _need(grad_w, "grad_w", _F32, (T, K))
     _need(grad_logits, "grad_logits", (logits.dtype,), (T, E))
-    with torch.cuda.device(_same_device(logits, grad_w, topk_idx, grad_logits)):
+    with _device_of(logits, grad_w, topk_idx, grad_logits):
         check("ep_route_backward", LIB.ep_route_backward(
             grad_w.data_ptr(), logits.data_ptr(), _logits_dtype(logits), topk_idx.data_ptr(), T, E, K, int(score),
             int(bool(renormalize)), float(scale), grad_logits.data_ptr(), _stream(stream)))
@@ -409,7 +420,7 @@ def ep_quantize_rows(x, format, q, scale, stream=None):
     if format not in (EP_RECV_FP8_E4M3_G128, EP_RECV_MXFP4_G32):
         raise ValueError("rows are quantised to FP8 or MXFP4, not format %r" % (format,))
     _need_recv(format, q, scale, R, H, ("q", "scale"))
-    with torch.cuda.device(_same_device(x, q, scale)):
+    with _device_of(x, q, scale):
         check("ep_quantize_rows", LIB.ep_quantize_rows(x.data_ptr(), R, H, int(format), q.data_ptr(),
                                                        scale.data_ptr(), _stream(stream)))
 
@@ -423,7 +434,7 @@ def ep_dequantize_rows(q, scale, format, x, stream=None):
     if format not in (EP_RECV_FP8_E4M3_G128, EP_RECV_MXFP4_G32):
         raise ValueError("rows are dequantised from FP8 or MXFP4, not format %r" % (format,))
     _need_recv(format, q, scale, R, H, ("q", "scale"))
-    with torch.cuda.device(_same_device(x, q, scale)):
+    with _device_of(x, q, scale):
         check("ep_dequantize_rows", LIB.ep_dequantize_rows(q.data_ptr(), scale.data_ptr(), R, H, int(format),
                                                            x.data_ptr(), _stream(stream)))
 
@@ -457,7 +468,7 @@ def ep_expert_product(a, a_scale, format, w, w_scale, expert_rows, capacity, act
     if N % (16 if activation == EP_ACT_SWIGLU else 8):
         raise ValueError("the product needs out channels in multiples of 8")
     _need(y, "y", _BF16, (R, N // 2 if activation == EP_ACT_SWIGLU else N))
-    with torch.cuda.device(_same_device(a, a_scale, w, w_scale, expert_rows, y)):
+    with _device_of(a, a_scale, w, w_scale, expert_rows, y):
         check("ep_expert_product", LIB.ep_expert_product(
             a.data_ptr(), a_scale.data_ptr(), int(format), w.data_ptr(), w_scale.data_ptr(), expert_rows.data_ptr(),
             R, E, cap, H, N, int(activation), y.data_ptr(), _stream(stream)))

@@ -40,162 +40,6 @@ __device__ __forceinline__ T wave_sum(T v) {
   return v;
 }
 
-// The lane holding the largest (key, lowest index) of the wavefront.
-__device__ __forceinline__ void wave_argmax(double& key, int& idx) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const double k = __shfl_xor(key, d);
-    const int i = __shfl_xor(idx, d);
-    if (k > key || (k == key && i < idx)) {
-      key = k;
-      idx = i;
-    }
-  }
-}
-
-struct RouteArgs {
-  const float* bias;
-  int32_t* ids;
-  float* weights;
-  int32_t T, E, K, n_group, topk_group, score, renorm;
-  float scale;
-};
-
-// One token in binary64, by a whole wavefront: the rule as it stands.  Lane l
-// holds experts l, l + 64, ..; EPL of them.  v_lds: E doubles of the wavefront.
-template <typename Z, int EPL>
-__device__ __attribute__((noinline)) void route_token(const Z* __restrict__ logits, const RouteArgs A, int t,
-                                                      double* v_lds) {
-  const float* bias = A.bias;
-  const int E = A.E, K = A.K, n_group = A.n_group, topk_group = A.topk_group, score = A.score;
-  const int lane = threadIdx.x & (kWave - 1);
-  const double ninf = -__builtin_inf();
-  float z[EPL];
-  float zmax = kNegInf;
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const int e = j * kWave + lane;
-    z[j] = e < E ? clean_logit(load_logit(logits + static_cast<size_t>(t) * E + e)) : kNegInf;
-    if (bias != nullptr && e < E && !(bias[e] > kNegInf)) z[j] = kNegInf;
-    zmax = fmaxf(zmax, z[j]);
-  }
-  zmax = wave_max(zmax);
-  double s[EPL], key[EPL], total = 0.0;
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const bool on = z[j] > kNegInf;
-    if (score == 1)
-      s[j] = on ? 1.0 / (1.0 + exp(-static_cast<double>(z[j]))) : 0.0;
-    else
-      s[j] = on ? exp(static_cast<double>(z[j]) - static_cast<double>(zmax)) : 0.0;
-    total += s[j];
-  }
-  if (score == 0) {
-    total = wave_sum(total);
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) s[j] = total > 0.0 ? s[j] / total : 0.0;
-  }
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const int e = j * kWave + lane;
-    const bool on = z[j] > kNegInf;
-    const double v = s[j] + (bias != nullptr && e < E ? static_cast<double>(bias[e]) : 0.0);
-    key[j] = !on ? ninf : (bias != nullptr ? v : static_cast<double>(z[j]));
-    if (e < E) v_lds[e] = on ? v : ninf;
-  }
-  if (n_group > 1) {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const int n = E / n_group;
-    double gs = ninf;
-    if (lane < n_group) {
-      double a = ninf, b = ninf;
-      for (int i = 0; i < n; ++i) {
-        const double v = v_lds[lane * n + i];
-        if (v > a) {
-          b = a;
-          a = v;
-        } else if (v > b) {
-          b = v;
-        }
-      }
-      if (a > ninf) gs = rint((b > ninf ? a + b : a) * 0x1p40);
-    }
-    int above = 0;
-    for (int g = 0; g < n_group; ++g) {
-      const double o = __shfl(gs, g);
-      above += o > gs || (o == gs && g < lane);
-    }
-    const uint64_t kept = wave_ballot(lane < n_group && above < topk_group);
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      const int e = j * kWave + lane;
-      if (e < E && !((kept >> (e / n)) & 1)) key[j] = ninf;
-    }
-  }
-  // the K best, one after the other; lane k keeps entry k
-  int my_id = -1;
-  float my_z = kNegInf;
-  double my_s = 0.0;
-  for (int k = 0; k < K; ++k) {
-    double best = ninf;
-    int at = 1 << 30;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (key[j] > best) {
-        best = key[j];
-        at = j * kWave + lane;
-      }
-    wave_argmax(best, at);
-    if (!(best > ninf)) break;
-    float bz = 0.0f;
-    double bs = 0.0;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (j * kWave + lane == at) {
-        key[j] = ninf;
-        bz = z[j];
-        bs = s[j];
-      }
-    bz = __shfl(bz, at & (kWave - 1));
-    bs = __shfl(bs, at & (kWave - 1));
-    if (lane == k) {
-      my_id = at;
-      my_z = bz;
-      my_s = bs;
-    }
-  }
-  if (A.renorm) {
-    // q = s / sum s, each s divided by exp(min(zmax of the chosen, 0)) first
-    // so that very negative logits do not underflow together
-    const double m = wave_max(my_z);
-    double u = 0.0;
-    if (my_id >= 0) {
-      const double zz = my_z;
-      u = score == 1 ? exp(fmin(zz, 0.0) - fmin(m, 0.0)) / (1.0 + exp(-fabs(zz))) : exp(zz - m);
-    }
-    my_s = u;
-    const double sum = wave_sum(u);
-    if (sum > 0.0) my_s = u / sum;
-  }
-  if (lane < K) {
-    A.ids[static_cast<size_t>(t) * K + lane] = my_id;
-    A.weights[static_cast<size_t>(t) * K + lane] = my_id >= 0 ? static_cast<float>(A.scale * my_s) : 0.0f;
-  }
-}
-
-// ---- the binary32 path --------------------------------------------------------
-//
-// LPT lanes per token (two tokens in a wavefront up to 256 experts), EPL
-// neighbouring experts in each lane, sorted there once; the K best are then
-// taken one by one: the largest head over the lanes (a butterfly of DPP and
-// lane swaps), and its lane drops it.  A lane holds neighbours in index order,
-// so the lowest lane among equal heads is the lowest index.
-//
-// Without a bias experts are compared by their logits, which is exact.  Group
-// scores, and scores with a bias, are compared in binary32; where two that
-// matter lie nearer than their rounding errors, the token is done again by
-// route_token.
-
 // Largest value of the LPT lanes, in all of them.
 template <int LPT>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
@@ -231,10 +75,183 @@ __device__ __forceinline__ float from_order(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// e^z with a relative error of a few units of binary32's last place.
+struct RouteArgs {
+  const float* bias;
+  int32_t* ids;
+  float* weights;
+  int32_t T, E, K, n_group, topk_group, score, renorm;
+  float scale;
+};
+
+// Binary64 values as unsigned numbers of the same order (0 below all of them).
+__device__ __forceinline__ uint64_t order_bits(double v) {
+  const int64_t u = __double_as_longlong(v + 0.0);
+  return static_cast<uint64_t>(u ^ ((u >> 63) | static_cast<int64_t>(0x8000000000000000ull)));
+}
+
+// Largest of the wavefront's values, in all lanes.
+__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
+  const uint32_t hi = lanes_max<64>(static_cast<uint32_t>(v >> 32));
+  const uint32_t lo = lanes_max<64>(static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+// One token in binary64, by a whole wavefront: the rule as it stands.  Lane l
+// holds experts l * EPL ..; v_lds: E doubles of the wavefront, sum_lds: room
+// for EP_MAX_GROUPS doubles.
+template <typename Z, int EPL>
+__device__ __attribute__((noinline)) void route_token(const Z* __restrict__ logits, const RouteArgs A, int t,
+                                                      double* v_lds, double* sum_lds) {
+  const int lane = threadIdx.x & (kWave - 1), E = A.E, e0 = lane * EPL;
+  const double ninf = -__builtin_inf();
+  float z[EPL], zmax = kNegInf;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const int e = e0 + j;
+    z[j] = e < E ? clean_logit(load_logit(logits + static_cast<size_t>(t) * E + e)) : kNegInf;
+    if (A.bias != nullptr && e < E && !(A.bias[e] > kNegInf)) z[j] = kNegInf;
+    zmax = fmaxf(zmax, z[j]);
+  }
+  double s[EPL], total = 0.0;
+  if (A.score == 0) zmax = wave_max(zmax);
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const double zz = z[j];
+    s[j] = !(z[j] > kNegInf) ? 0.0 : (A.score == 1 ? 1.0 / (1.0 + exp(-zz)) : exp(zz - static_cast<double>(zmax)));
+    total += s[j];
+  }
+  if (A.score == 0) {
+    total = wave_sum(total);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) s[j] = total > 0.0 ? s[j] / total : 0.0;
+  }
+  uint64_t key[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const bool on = z[j] > kNegInf;
+    const double v = s[j] + (A.bias != nullptr && e0 + j < E ? static_cast<double>(A.bias[e0 + j]) : 0.0);
+    key[j] = !on ? 0 : order_bits(A.bias != nullptr ? v : static_cast<double>(z[j]));
+    if (e0 + j < E) v_lds[e0 + j] = on ? v : ninf;
+  }
+  if (A.n_group > 1) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int n = E / A.n_group;
+    int P = 1;  // lanes per group
+    while (P * 2 * A.n_group <= kWave) P *= 2;
+    double a = ninf, b = ninf;
+    const int g = lane / P;
+    if (g < A.n_group)
+      for (int i = lane & (P - 1); i < n; i += P) {
+        const double v = v_lds[g * n + i];
+        b = fmax(b, fmin(a, v));
+        a = fmax(a, v);
+      }
+    for (int d = 1; d < P; d <<= 1) {
+      const double oa = __shfl_xor(a, d), ob = __shfl_xor(b, d);
+      b = fmax(fmax(b, ob), fmin(a, oa));
+      a = fmax(a, oa);
+    }
+    const double gs = a > ninf ? rint((b > ninf ? a + b : a) * 0x1p40) : ninf;
+    if (g < A.n_group && (lane & (P - 1)) == 0) sum_lds[g] = gs;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const double mine = lane < A.n_group ? sum_lds[lane] : ninf;
+    int above = 0;
+    for (int o = 0; o < A.n_group; ++o) {
+      const double x = sum_lds[o];
+      above += x > mine || (x == mine && o < lane);
+    }
+    const uint64_t kept = wave_ballot(lane < A.n_group && mine > ninf && above < A.topk_group);
+    int ge = e0 / n, r = e0 - ge * n;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      if (!((kept >> (ge & 63)) & 1)) key[j] = 0;
+      if (++r == n) {
+        r = 0;
+        ++ge;
+      }
+    }
+  }
+  // the K best, one after the other; the winner's lane hands its values to
+  // lane k (a lane holds neighbours in index order: the lowest lane among
+  // equal keys is the lowest index)
+  int my_id = -1;
+  float my_z = kNegInf;
+  double my_s = 0.0;
+  for (int k = 0; k < A.K; ++k) {
+    uint64_t best = 0;
+    int at = 0;
+    float bz = 0.0f;
+    double bs = 0.0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        at = j;
+        bz = z[j];
+        bs = s[j];
+      }
+    const uint64_t m = wave_max_u64(best);
+    if (m == 0) break;
+    const int w = __builtin_ctzll(wave_ballot(best == m));
+    if (lane == w) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j)
+        if (j == at) key[j] = 0;
+    }
+    const int id = __shfl(e0 + at, w);
+    bz = __shfl(bz, w);
+    bs = __shfl(bs, w);
+    if (lane == k) {
+      my_id = id;
+      my_z = bz;
+      my_s = bs;
+    }
+  }
+  if (A.renorm) {
+    // q = s / sum s, each s divided by exp(min(zmax of the chosen, 0)) first
+    // so that very negative logits do not underflow together
+    const double m = wave_max(my_z);
+    double u = 0.0;
+    if (my_id >= 0) {
+      const double zz = my_z;
+      u = A.score == 1 ? exp(fmin(zz, 0.0) - fmin(m, 0.0)) / (1.0 + exp(-fabs(zz))) : exp(zz - m);
+    }
+    my_s = u;
+    const double sum = wave_sum(u);
+    if (sum > 0.0) my_s = u / sum;
+  }
+  if (lane < A.K) {
+    A.ids[static_cast<size_t>(t) * A.K + lane] = my_id;
+    A.weights[static_cast<size_t>(t) * A.K + lane] = my_id >= 0 ? static_cast<float>(A.scale * my_s) : 0.0f;
+  }
+}
+
+// ---- the binary32 path --------------------------------------------------------
+//
+// LPT lanes per token (two tokens in a wavefront up to 256 experts), EPL
+// neighbouring experts in each lane, sorted there once; the K best are then
+// taken one by one: the largest head over the lanes (a butterfly of DPP and
+// lane swaps), and its lane drops it.  A lane holds neighbours in index order,
+// so the lowest lane among equal heads is the lowest index.
+//
+// Without a bias experts are compared by their logits, which is exact.  Group
+// scores, and scores with a bias, are compared in binary32; where two that
+// matter lie nearer than their rounding errors, the token is done again by
+// route_token.
+
+// e^z within a few units of binary32's last place (0 where it leaves the
+// normal range): exp2 of z log2(e), whose rounding error is put back.
+__device__ __forceinline__ float exp32(float z) {
+  const float y = z * 0x1.715476p+0f;
+  const float r = __builtin_fmaf(z, 0x1.4ae0bep-26f, __builtin_fmaf(z, 0x1.715476p+0f, -y));
+  const float e = __builtin_amdgcn_exp2f(y);
+  return __builtin_fmaf(e * r, 0x1.62e430p-1f, e);
+}
+
+// 1 / (1 + e^-z), likewise.
 __device__ __forceinline__ float sigmoid32(float z) {
-  const float e = expf(-fabsf(z));
-  return (z >= 0.0f ? 1.0f : e) / (1.0f + e);
+  const float e = exp32(fmaxf(-fabsf(z), -150.0f));
+  return (z >= 0.0f ? 1.0f : e) * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 template <int EPL>
@@ -297,7 +314,7 @@ __device__ __forceinline__ void load_logits(const uint16_t* p, int n, bool vec, 
 }
 
 template <typename Z, int EPL, int LPT, bool BIAS>
-__global__ __launch_bounds__(kThreads) void route_kernel(const Z* __restrict__ logits, RouteArgs A, bool vec) {
+__global__ __launch_bounds__(kThreads) void route_kernel(const Z* __restrict__ logits, RouteArgs A, bool vec, bool vec_bias) {
   extern __shared__ double route_lds[];  // per wave: E doubles (route_token; the groups' scan of binary32 keys)
   constexpr int TPW = kWave / LPT;       // tokens per wavefront
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
@@ -307,17 +324,25 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const Z* __restrict__ l
   if (t0 >= A.T) return;  // no barrier below: the wavefronts are independent
   const int t = min(t0 + half, A.T - 1);  // (the last token twice where T is odd)
   double* v_lds = route_lds + static_cast<size_t>(wave) * E;
+  // ids of the wave's tokens, 2 x EP_MAX_TOPK (before that their groups' sums, 2 x EP_MAX_GROUPS)
+  int* id_lds = reinterpret_cast<int*>(route_lds + static_cast<size_t>(kWaves) * E) + wave * 2 * EP_MAX_GROUPS + half * EP_MAX_TOPK;
   const int e0 = sub * EPL;
   float z[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) z[j] = kNegInf;
   load_logits<EPL>(logits + static_cast<size_t>(t) * E + e0, E - e0, vec, z);
+  float bias[EPL];
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) bias[j] = 0.0f;
+    load_logits<EPL>(A.bias + e0, E - e0, vec_bias, bias);
+  }
   bool near = false;  // a comparison that binary32 cannot decide
   float zmax = kNegInf, inv = 0.0f;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     z[j] = clean_logit(z[j]);
-    if (BIAS && e0 + j < E && !(A.bias[e0 + j] > kNegInf)) z[j] = kNegInf;
+    if (BIAS && !(bias[j] > kNegInf)) z[j] = kNegInf;
     zmax = fmaxf(zmax, z[j]);
   }
   const bool softmax = A.score == 0;
@@ -325,144 +350,168 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const Z* __restrict__ l
     zmax = from_order(max(lanes_max<LPT>(order_bits(zmax)), 0x00800000u));
     float sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) sum += z[j] > kNegInf ? expf(z[j] - zmax) : 0.0f;
+    for (int j = 0; j < EPL; ++j) sum += exp32(fmaxf(z[j] - zmax, -150.0f));  // (0 for -inf)
     sum = lanes_sum<LPT>(sum);
     inv = sum > 0.0f ? 1.0f / sum : 0.0f;
   }
   const auto score_of = [&](float x) {
-    return !(x > kNegInf) ? 0.0f : (softmax ? expf(x - zmax) * inv : sigmoid32(x));
+    return softmax ? exp32(fmaxf(x - zmax, -150.0f)) * inv : sigmoid32(x);
   };
   // (key, index from behind): largest first, ties to the lower index; 0: off
   uint64_t k[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
-    const float v = BIAS && e0 + j < E ? score_of(z[j]) + A.bias[e0 + j] : z[j];
+    const float v = BIAS ? score_of(z[j]) + bias[j] : z[j];
     k[j] = z[j] > kNegInf ? static_cast<uint64_t>(order_bits(v)) << 32 | static_cast<uint32_t>(EPL - 1 - j) : 0;
   }
 
+  // Groups of whole lanes, a power of two of them, have their two largest in
+  // the sorted lanes' heads; others go through LDS and are sorted afterwards.
+  const int n = A.n_group > 1 ? E / A.n_group : E;
+  const int lanes = n / EPL;  // lanes per group
+  const bool whole = n % EPL == 0 && (lanes & (lanes - 1)) == 0 && lanes <= 16;
+  if (whole || A.n_group == 1) sort_desc(k);
   if (A.n_group > 1) {
-    // two largest of each group, by the lanes of a token in turn over groups
-    const int n = E / A.n_group;
-    uint32_t* key_lds = reinterpret_cast<uint32_t*>(v_lds) + half * E;  // 2 E words a wavefront
-#pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (e0 + j < E) key_lds[e0 + j] = static_cast<uint32_t>(k[j] >> 32);
+    uint32_t* sum_lds = reinterpret_cast<uint32_t*>(id_lds) - half * EP_MAX_TOPK + half * EP_MAX_GROUPS;
+    for (int g = sub; g < EP_MAX_GROUPS; g += LPT) sum_lds[g] = 0;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    // P lanes per group, P a power of two; rounds where LPT lanes are too few
-    float mine = 0.0f;   // the score of group `sub` (and of sub + LPT where LPT < n_group)
-    float mine2 = 0.0f;
-    float mag = 1.0f;    // largest magnitude that goes into a score
-    bool any = false, any2 = false;
-    int P = 1;
-    while (P * 2 * A.n_group <= LPT && P < 16) P *= 2;
-    for (int g0 = 0; g0 < A.n_group; g0 += LPT / P) {
-      const int g = g0 + sub / P;
-      uint32_t b0 = 0, b1 = 0;
-      if (g < A.n_group)
-        for (int i = sub & (P - 1); i < n; i += P) {
-          const uint32_t x = key_lds[g * n + i];
-          b1 = max(b1, min(b0, x));
-          b0 = max(b0, x);
-        }
-      for (int d = 1; d < P; d <<= 1) {
-        const uint32_t o0 = __shfl_xor(b0, d), o1 = __shfl_xor(b1, d);
-        b1 = max(max(b1, o1), min(b0, o0));
-        b0 = max(b0, o0);
-      }
-      float gs = 0.0f;
-      if (b0) gs += BIAS ? from_order(b0) : score_of(from_order(b0));
-      if (b1) gs += BIAS ? from_order(b1) : score_of(from_order(b1));
-      if (BIAS) {
-        if (b0) mag = fmaxf(mag, fabsf(from_order(b0)));
-        if (b1) mag = fmaxf(mag, fabsf(from_order(b1)));
-      }
-      // group g's score to lane g (of the token)
-      const int src = (lane & ~(LPT - 1)) + ((sub - g0) * P & (LPT - 1));
-      const float got = __shfl(gs, src);
-      const bool on = __shfl(static_cast<int>(b0 != 0), src) != 0;
-      if (sub >= g0 && sub < g0 + LPT / P && sub < A.n_group) {
-        mine = got;
-        any = on;
-      }
-      if (LPT < 64 && sub + LPT >= g0 && sub + LPT < g0 + LPT / P && sub + LPT < A.n_group) {
-        mine2 = got;
-        any2 = on;
-      }
-    }
-    // each lane ranks its group (its two groups)
-    int above = 0, above2 = 0;
-    const auto beats = [](float a, bool ao, int ai, float b, bool bo, int bi) {
-      return ao && (!bo || a > b || (a == b && ai < bi));
+    float mag = 1.0f;  // largest magnitude that goes into a sum
+    // the sum of a group's two largest, as order bits (0: nobody to choose)
+    const auto add_up = [&](uint32_t b0, uint32_t b1) {
+      const float v0 = from_order(b0), v1 = from_order(b1);
+      float gs = BIAS ? v0 : score_of(v0);
+      if (b1 != 0) gs += BIAS ? v1 : score_of(v1);
+      if (BIAS && b0 != 0) mag = fmaxf(fmaxf(mag, fabsf(v0)), b1 != 0 ? fabsf(v1) : 0.0f);
+      return b0 != 0 ? order_bits(gs) : 0u;
     };
-    for (int g = 0; g < A.n_group; ++g) {
-      const int src = (lane & ~(LPT - 1)) + (g & (LPT - 1));
-      const float o = g < LPT ? __shfl(mine, src) : __shfl(mine2, src);
-      const bool oo = (g < LPT ? __shfl(static_cast<int>(any), src) : __shfl(static_cast<int>(any2), src)) != 0;
-      above += beats(o, oo, g, mine, any, sub);
-      above2 += beats(o, oo, g, mine2, any2, sub + LPT);
+    uint32_t b0 = 0, b1 = 0;
+    const auto merge = [&](auto ctrl) {
+      constexpr int C = decltype(ctrl)::value;
+      const uint32_t o0 = __builtin_amdgcn_update_dpp(0, static_cast<int>(b0), C, 0xF, 0xF, false);
+      const uint32_t o1 = __builtin_amdgcn_update_dpp(0, static_cast<int>(b1), C, 0xF, 0xF, false);
+      b1 = max(max(b1, o1), min(b0, o0));
+      b0 = max(b0, o0);
+    };
+    if (whole) {
+      b0 = static_cast<uint32_t>(k[0] >> 32);
+      b1 = EPL > 1 ? static_cast<uint32_t>(k[EPL > 1 ? 1 : 0] >> 32) : 0;
+      if (lanes >= 2) merge(std::integral_constant<int, 0xB1>{});
+      if (lanes >= 4) merge(std::integral_constant<int, 0x4E>{});
+      if (lanes >= 8) merge(std::integral_constant<int, 0x141>{});
+      if (lanes >= 16) merge(std::integral_constant<int, 0x140>{});
+      const uint32_t sum = add_up(b0, b1);
+      if (e0 < E && (sub & (lanes - 1)) == 0) sum_lds[sub / lanes] = sum;
+    } else {
+      uint32_t* key_lds = reinterpret_cast<uint32_t*>(v_lds) + half * E;  // 2 E words a wavefront
+#pragma unroll
+      for (int j = 0; j < EPL; ++j)
+        if (e0 + j < E) key_lds[e0 + j] = static_cast<uint32_t>(k[j] >> 32);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      // P neighbouring lanes per group, in rounds where a token's lanes are too few
+      const int P = A.n_group * 4 <= LPT ? 4 : (A.n_group * 2 <= LPT ? 2 : 1);
+      for (int g0 = 0; g0 < A.n_group; g0 += LPT / P) {
+        const int g = g0 + sub / P;
+        b0 = b1 = 0;
+        if (g < A.n_group)
+          for (int i = sub & (P - 1); i < n; i += P) {
+            const uint32_t x = key_lds[g * n + i];
+            b1 = max(b1, min(b0, x));
+            b0 = max(b0, x);
+          }
+        if (P >= 2) merge(std::integral_constant<int, 0xB1>{});
+        if (P >= 4) merge(std::integral_constant<int, 0x4E>{});
+        const uint32_t sum = add_up(b0, b1);
+        if (g < A.n_group && (sub & (P - 1)) == 0) sum_lds[g] = sum;
+      }
     }
-    const bool keep = sub < A.n_group && any && above < A.topk_group;
-    const bool keep2 = LPT < 64 && sub + LPT < A.n_group && any2 && above2 < A.topk_group;
-    const uint64_t m1 = wave_ballot(keep), m2 = wave_ballot(keep2);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // each lane ranks group `sub` (and sub + LPT): how many come before it
+    const bool more = LPT < EP_MAX_GROUPS && A.n_group > LPT;
+    const uint32_t mine = sum_lds[sub], mine2 = more ? sum_lds[(sub + LPT) % EP_MAX_GROUPS] : 0;
+    int above = 0, above2 = 0;
+    for (int g = 0; g < A.n_group; g += 4) {  // (sums past the last group are 0)
+      const u32x4 o = *reinterpret_cast<const u32x4*>(sum_lds + g);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {  // a tie goes to the lower group
+        above += o[x] > mine - (g + x < sub ? 1u : 0u);
+        if (more) above2 += o[x] > mine2 - (g + x < sub + LPT ? 1u : 0u);
+      }
+    }
+    const bool keep = mine != 0 && above < A.topk_group;
+    const bool keep2 = mine2 != 0 && above2 < A.topk_group;
+    const uint64_t m1 = wave_ballot(keep), m2 = more ? wave_ballot(keep2) : 0;
     const uint64_t kept = LPT == 64 ? m1 : ((m1 >> (half * 32)) & 0xFFFFFFFFull) | (m2 >> (half * 32)) << 32;
-    // the last kept score against the first dropped one
-    const uint32_t low_bits = ~0u;
-    uint32_t worst = 0, best = 0;  // order bits; the smallest kept as the largest complement
-    if (sub < A.n_group && any) (keep ? worst : best) = keep ? low_bits - order_bits(mine) : order_bits(mine);
-    if (LPT < 64 && sub + LPT < A.n_group && any2) {
-      if (keep2) worst = max(worst, low_bits - order_bits(mine2));
-      else best = max(best, order_bits(mine2));
-    }
-    worst = lanes_max<LPT>(worst);
-    best = lanes_max<LPT>(best);
+    // the last kept sum against the first dropped one: the smallest kept as
+    // the largest complement
+    const uint32_t worst = lanes_max<LPT>(max(keep ? ~mine : 0u, keep2 ? ~mine2 : 0u));
+    const uint32_t best = lanes_max<LPT>(max(keep ? 0u : mine, keep2 ? 0u : mine2));
+    if (BIAS) mag = from_order(lanes_max<LPT>(order_bits(mag)));
     if (best != 0) {
-      const float lo = from_order(low_bits - worst), hi = from_order(best);
-      // binary32 is off by a few units of 2^-24 of what is added up, the rule's
-      // own rounding by half of 2^-40
-      if (BIAS) mag = from_order(lanes_max<LPT>(order_bits(mag)));
+      const float lo = from_order(~worst), hi = from_order(best);
+      // each score is off by at most 2^-21.6 of itself (2^-22 + 2^-24 with a
+      // bias), the rule's own rounding by half of 2^-40
       near = lo - hi <= (BIAS ? 0x1p-19f * mag : 0x1p-19f * fmaxf(lo, hi) + 0x1p-38f);
     }
+    if (whole) {
+      if (!((kept >> (sub / lanes & 63)) & 1)) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j)
-      if (e0 + j < E && !((kept >> ((e0 + j) / n)) & 1)) k[j] = 0;
+        for (int j = 0; j < EPL; ++j) k[j] = 0;
+      }
+    } else {
+      int g = e0 / n, r = e0 - g * n;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        if (!((kept >> (g & 63)) & 1)) k[j] = 0;
+        if (++r == n) {
+          r = 0;
+          ++g;
+        }
+      }
+      sort_desc(k);
+    }
   }
-
-  sort_desc(k);
 
   // the K best (with a bias one more, for the last comparison); lane i of the
   // token keeps entry i's key, the winner's lane writes its index
-  int* id_lds = reinterpret_cast<int*>(route_lds + static_cast<size_t>(kWaves) * E) + (wave * 2 + half) * EP_MAX_TOPK;
-  if (sub < K && sub < EP_MAX_TOPK) id_lds[sub] = -1;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if (sub < K) id_lds[sub] = -1;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   uint32_t my_key = 0, before = 0;
   bool tie = false;
+  uint32_t head[EPL];  // the sorted keys, and their places in the lane, four bits each
+  uint64_t place = 0;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    head[j] = static_cast<uint32_t>(k[j] >> 32);
+    place |= static_cast<uint64_t>((EPL - 1 - static_cast<uint32_t>(k[j])) & 15) << (4 * j);
+  }
   for (int i = 0; i < K + (BIAS ? 1 : 0); ++i) {
-    const uint32_t head = static_cast<uint32_t>(k[0] >> 32);
-    const uint32_t m = lanes_max<LPT>(head);
-    const bool eq = head == m && m != 0;
+    const uint32_t m = lanes_max<LPT>(head[0]);
+    const bool eq = head[0] == m && m != 0;
     const uint64_t mask = wave_ballot(eq);
     const uint32_t lower = LPT == 64 ? lanes_below(mask)
                                      : (half ? __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32), 0u)
                                              : __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0u));
-    const bool win = eq && lower == 0;
     if (BIAS && i > 0 && m != 0 && before != 0) {
       const float hi = from_order(before), lo = from_order(m);
+      // a score is off by at most 2^-22, and by 2^-24 of its sum with the bias
       tie = tie || hi - lo <= 0x1p-20f * fmaxf(1.0f, fmaxf(fabsf(hi), fabsf(lo)));
     }
     before = m;
     if (i == K) break;
-    if (win) {
-      id_lds[i] = e0 + EPL - 1 - static_cast<int>(static_cast<uint32_t>(k[0]));
+    if (eq && lower == 0) {
+      id_lds[i] = e0 + static_cast<int>(static_cast<uint32_t>(place) & 15);
 #pragma unroll
-      for (int j = 0; j + 1 < EPL; ++j) k[j] = k[j + 1];
-      k[EPL - 1] = 0;
+      for (int j = 0; j + 1 < EPL; ++j) head[j] = head[j + 1];
+      head[EPL - 1] = 0;
+      if (EPL <= 8) place = static_cast<uint32_t>(place) >> 4; else place >>= 4;
     }
     my_key = sub == i ? m : my_key;
   }
   near = near || tie;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 
-  const int id = sub < K && sub < EP_MAX_TOPK ? id_lds[sub] : -1;
+  const int id = sub < K ? id_lds[sub] : -1;
   float zk = kNegInf;
   if (id >= 0) zk = BIAS ? clean_logit(load_logit(logits + static_cast<size_t>(t) * E + id)) : from_order(my_key);
   float q = 0.0f;
@@ -470,9 +519,12 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const Z* __restrict__ l
     // s / sum s, each s divided by exp(min(largest chosen logit, 0)) first so
     // that very negative logits do not underflow together
     const float m = from_order(max(lanes_max<LPT>(order_bits(zk)), 0x00800000u));
-    if (id >= 0) q = softmax ? expf(zk - m) : expf(fminf(zk, 0.0f) - fminf(m, 0.0f)) / (1.0f + expf(-fabsf(zk)));
+    if (id >= 0) {
+      q = exp32(fmaxf(softmax ? zk - m : fminf(zk, 0.0f) - fminf(m, 0.0f), -150.0f));
+      if (!softmax) q *= __builtin_amdgcn_rcpf(1.0f + exp32(fmaxf(-fabsf(zk), -150.0f)));
+    }
     const float sum = lanes_sum<LPT>(q);
-    if (sum > 0.0f) q /= sum;
+    if (sum > 0.0f) q *= __builtin_amdgcn_rcpf(sum);
   } else if (id >= 0) {
     q = score_of(zk);
   }
@@ -485,7 +537,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const Z* __restrict__ l
   for (int h = 0; h < TPW; ++h) {
     if (((again >> (h * 32)) & 1) == 0 || t0 + h >= A.T) continue;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    route_token<Z, (EPL * LPT + kWave - 1) / kWave>(logits, A, t0 + h, v_lds);
+    route_token<Z, (EPL * LPT + kWave - 1) / kWave>(logits, A, t0 + h, v_lds,
+                                                    reinterpret_cast<double*>(id_lds - half * EP_MAX_TOPK));
   }
 }
 
@@ -572,16 +625,18 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
 
 template <typename Z>
 hipError_t route(const Z* logits, const RouteArgs& A, hipStream_t stream) {
-  // per wave: E doubles, and the ids of its tokens
-  const size_t lds = static_cast<size_t>(kWaves) * (A.E * sizeof(double) + 2 * EP_MAX_TOPK * sizeof(int));
+  // per wave: E doubles, and the groups' sums or the ids of its tokens
+  const size_t lds = static_cast<size_t>(kWaves) * (A.E * sizeof(double) + 2 * EP_MAX_GROUPS * sizeof(int));
+  static_assert(EP_MAX_TOPK <= EP_MAX_GROUPS && EP_MAX_TOPK <= 32, "a lane per entry");
   const auto launch = [&](auto epl, auto lpt) {
     constexpr int EPL = decltype(epl)::value, LPT = decltype(lpt)::value, tokens = kWaves * (kWave / LPT);
     const dim3 grid((A.T + tokens - 1) / tokens), block(kThreads);
     const bool vec = A.E % EPL == 0 && A.E * sizeof(Z) % 16 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
+    const bool vec_bias = A.E % EPL == 0 && EPL % 4 == 0 && (reinterpret_cast<uintptr_t>(A.bias) & 15) == 0;
     if (A.bias != nullptr)
-      hipLaunchKernelGGL((route_kernel<Z, EPL, LPT, true>), grid, block, lds, stream, logits, A, vec);
+      hipLaunchKernelGGL((route_kernel<Z, EPL, LPT, true>), grid, block, lds, stream, logits, A, vec, vec_bias);
     else
-      hipLaunchKernelGGL((route_kernel<Z, EPL, LPT, false>), grid, block, lds, stream, logits, A, vec);
+      hipLaunchKernelGGL((route_kernel<Z, EPL, LPT, false>), grid, block, lds, stream, logits, A, vec, vec_bias);
     return hipGetLastError();
   };
   const std::integral_constant<int, 32> two{};
