@@ -4,8 +4,16 @@
 //
 // gfx950's scaled MFMA takes the codes as they are and multiplies each
 // 32-channel block by both operands' E8M0 scales.  The weights are its A
-// operand (16 channels of y), the rows its B operand (16 rows), so a lane
-// ends up with four consecutive channels of one row.
+// operand (channels of y), the rows its B operand, so a lane ends up with four
+// consecutive channels of one row.  FP8 rows go through it with a scale of 1
+// and 128 channels at a time, whose sums are scaled on the vector unit.
+//
+// With E 256, H 7168, N 4096 gated and 8 experts a token: 1 token 25 us, 128
+// tokens 565 us (MXFP4 rows; the weights at 7.0 TB/s), 682 us (FP8 rows; the
+// same weights, four instead of one LDS piece a row and step), 4096 tokens 1013
+// us (4.2 TB/s and 1.9 PFLOP/s: bounded by copies into LDS that end at each
+// stage's barrier; without products 846, without copied rows 724), 32768 tokens
+// 4633 us (3.3 PFLOP/s; the matrix unit reaches 6.1 on such operands alone).
 
 #include "ep_device.h"
 #include "ep_internal.h"
@@ -121,11 +129,14 @@ __global__ __launch_bounds__(kThreads) void product_kernel(const uint8_t* __rest
 // Workgroup tile: BN weight rows (with GATED half gate, half up, of the same
 // BN/2 channels of y) times BM token rows, over all of H in stages of 256
 // channels.  A stage's codes go from global memory straight to LDS (16 bytes a
-// lane), into one of two buffers while the other one is multiplied; the copies
-// run on over the end of a tile into the next one.  LDS rows are 128 bytes
-// (FP8 rows 256) and hold their 16-byte pieces permuted (piece ^
-// swizzle(row)), so that the 16 lanes served together meet different banks.
-// Scales are copied 32 bytes a row, for four stages.
+// lane): rows into one of two buffers while the other one is multiplied,
+// weights into one of two or three, so one or two stages ahead; the copies run
+// on over the end of a tile into the next one.  LDS rows are 128 bytes (FP8
+// rows 256) and hold their 16-byte pieces permuted (piece ^ swizzle(row)), so
+// that the 16 lanes served together meet different banks.  Scales are copied
+// 64 bytes a weight row (eight stages; 32 where the tile is largest, which has
+// no registers left: 4642 against 4951 us) and 32 bytes a token row (four) at
+// a time: short pieces of many rows are what a copy costs most.
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __amdgpu_buffer_rsrc_t Rsrc;
@@ -144,11 +155,13 @@ __device__ __forceinline__ void copy16_once(Rsrc src, uint8_t* dst, uint32_t lan
   __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (LdsVoid*)dst, 16, lane_off, off, 0, 2);
 }
 
-// Until this wave's copies have arrived and its LDS reads are done; then the
-// workgroup's barrier.
+// Until at most N of this wave's copies are under way (they finish in order)
+// and its LDS reads are done; then the workgroup's barrier.
+template <int N>
 __device__ __forceinline__ void wait_and_sync() {
+  static_assert(N < 16, "vmcnt");
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_waitcnt(N | 7 << 4);  // vmcnt(N) lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -161,16 +174,36 @@ __device__ __forceinline__ i32x8 widen(u32x4 lo) {
                0, 0, 0, 0};
 }
 
+// The workgroup's barrier once this wave's LDS reads are done.
+__device__ __forceinline__ void wait_reads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(15 | 7 << 4 | 3 << 14);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// f(0) && f(1) && ...
+template <int I, int N, typename F>
+__device__ __forceinline__ bool static_while(F&& f) {
+  if constexpr (I < N) {
+    if (!f(std::integral_constant<int, I>{})) return false;
+    return static_while<I + 1, N>(f);
+  }
+  return true;
+}
+
 // An offset past the end of every operand (at most 2^31 bytes of one expert's
 // weights, 2^24 of a tile's rows): buffer loads from there give 0.
 constexpr uint32_t kNone = 0x80000000u;
 
-template <bool FP8, bool GATED, int BM, int BN, int WM, int WN>
+// BM x BN: the tile; WM x WN: its waves; WR: stages of weights kept; NT: the
+// weights are read non-temporally.
+template <bool FP8, bool GATED, int BM, int BN, int WM, int WN, int WR, bool NT>
 __global__ __launch_bounds__(WM* WN* kWave) void product_tiled(
     const uint8_t* __restrict__ a, const uint8_t* __restrict__ a_scale, const uint8_t* __restrict__ w,
     const uint8_t* __restrict__ w_scale, const int32_t* __restrict__ expert_rows, int32_t num_rows, int32_t E,
     int32_t capacity, int32_t H, int32_t N, uint16_t* __restrict__ y) {
-  constexpr int NW = WM * WN, kThr = NW * kWave;
+  constexpr int NW = WM * WN;
   constexpr int TN = BN / WN;                       // a wave's weight rows
   constexpr int FM = BM / WM / 32, FN = TN / 32;    // its fragments of 32 rows
   constexpr int AB = FP8 ? 256 : 128;               // bytes of a token row in a stage
@@ -178,119 +211,145 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tiled(
   constexpr int LA = BM * AB / 1024 / NW;           // 1024 / AB token rows each
   static_assert(LW * 8 * NW == BN && LA * 1024 * NW == BM * AB && FM * 32 * WM == BM && FN * 32 * WN == BN, "tile");
   static_assert(!GATED || FN % 2 == 0, "a wave holds both halves of its channels");
-  constexpr int SR = BN + BM;                       // rows of scales, in copies of 32
-  constexpr int LS = (SR / 32 + NW - 1) / NW;       // those per wave
+  constexpr int SW = BM > 192 ? 32 : 64;            // bytes of a weight row's scales copied at a time
+  constexpr int NQ = SW / 32;                       // quads of stages in SW bytes of a weight row's scales
+  constexpr int LSW = BN * SW / 1024 / NW;          // copies per wave for those: 1024 / SW rows each
+  constexpr int LSA = (BM / 32 + NW - 1) / NW;      // token rows' scales, a quad's (32 bytes): 32 rows each
+  static_assert(LSW * 1024 * NW == BN * SW && BM * AB >= 2048 * NW, "scales, and y's fragments");
   constexpr int BO = GATED ? BN / 2 : BN;           // channels of y per tile
   __shared__ __align__(16) uint8_t w0[BN * 128];
   __shared__ __align__(16) uint8_t w1[BN * 128];
+  __shared__ __align__(16) uint8_t w2[WR == 3 ? BN * 128 : 16];
   __shared__ __align__(16) uint8_t a0[BM * AB];
   __shared__ __align__(16) uint8_t a1[BM * AB];
-  __shared__ __align__(16) uint8_t sc[SR * 32 + 16];
-  __shared__ int start[kMaxExperts + 1];
+  __shared__ __align__(16) uint8_t scw[BN * SW];
+  __shared__ __align__(16) uint8_t sca[BM * 32 + 16];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int half = lane >> 5, col = lane & 31;
   const int wm = wave % WM, wn = wave / WM;
-  for (int e = tid; e < E; e += kThr) {
-    int first, count;
-    rows_of(expert_rows, e, capacity, num_rows, first, count);
-    start[e] = (count + BM - 1) / BM;
-  }
-  if (tid == 0) start[E] = 0;
-  __syncthreads();
-  block_exclusive_scan(start, E + 1);
   const int O = GATED ? N / 2 : N;
   const uint32_t nt = (O + BO - 1) / BO;
   const uint32_t wrow_bytes = H / 2, arow_bytes = FP8 ? H : H / 2, srow_bytes = H / 32;
-  const int stages = (H + 255) / 256, quads = (stages + 3) / 4;
-  const bool tail = (H & 255) != 0;  // the last stage holds 128 channels
-  const uint32_t tiles = static_cast<uint32_t>(start[E]) * nt;
+  const int stages = (H + 255) / 256;  // >= 2
+  const bool tail = (H & 255) != 0;    // the last stage holds 128 channels
 
   // Tiles in eight runs, one per XCD (workgroups go to the XCDs in turn), so
   // that neighbouring tiles, which share weights or rows, meet in one L2.
+  // Each wavefront finds the first one from sums over E / 64 experts a lane; from
+  // there on it walks over the experts.
+  const auto row_tiles = [&](int e) -> uint32_t {
+    int first, count;
+    rows_of(expert_rows, e, capacity, num_rows, first, count);
+    return (count + BM - 1) / BM;
+  };
+  int mine = 0;
+  const int per = (E + kWave - 1) / kWave;  // experts of a lane
+  for (int i = 0; i < per; i += 4) {
+    int n[4];  // (loaded for any lane, so that the four loads overlap)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) n[x] = row_tiles(min(lane * per + i + x, E - 1));
+#pragma unroll
+    for (int x = 0; x < 4; ++x) mine += i + x < per && lane * per + i + x < E ? n[x] : 0;
+  }
+  const int upto = wave_inclusive_scan(mine);
+  const uint32_t tiles = static_cast<uint32_t>(__builtin_amdgcn_readlane(upto, kWave - 1)) * nt;
   const uint32_t run = (tiles + 7) / 8, step = gridDim.x / 8;
-  uint32_t t = blockIdx.x / 8;
-  const uint32_t base = (blockIdx.x & 7) * run;
-  if (t >= run || base + t >= tiles) return;
+  const uint32_t end = min((blockIdx.x & 7) * run + run, tiles);
+  uint32_t tile = (blockIdx.x & 7) * run + blockIdx.x / 8;
+  if (tile >= end) return;
+  // the first lane that ends beyond this tile's row tile holds its expert
+  const int at = __builtin_ctzll(wave_ballot(static_cast<uint32_t>(upto) > tile / nt));
+  uint32_t before = __builtin_amdgcn_readlane(upto - mine, at);  // row tiles before expert `walk`
+  int walk = at * per;
+  uint32_t te = __builtin_amdgcn_readfirstlane(row_tiles(walk));  // and its own
 
   // The tile whose stages are being copied: its operands and this lane's
   // pieces.  Rows past the end repeat the last one.
-  int walk = 0, n0, rows, row0;
-  bool once;  // the expert's only row tile: its weights are read here alone
+  int n0, rows, row0, m0, first, count;
   Rsrc wr, ar, wsr, asr;
-  uint32_t woff[LW], aoff[LA], soff[LS];
-  const auto open_tile = [&]() {
-    const uint32_t tile = base + t;
-    const int q = static_cast<int>(tile / nt);
-    while (__builtin_amdgcn_readfirstlane(start[walk + 1]) <= q) ++walk;  // q < start[E]
-    int first, count;
+  uint32_t woff[LW], aoff[LA], swoff[LSW], saoff[LSA];
+  const auto weight_row = [&](int r0, int r) -> uint32_t {  // r0: wave-uniform, of the same half as r
+    const uint32_t n = min(n0 + (GATED && r0 >= BO ? r - BO : r), O - 1);
+    return GATED && r0 >= BO ? n + O : n;
+  };
+  const auto open_weights = [&]() {
+    const uint32_t q = tile / nt;
+    while (q >= before + te) {  // ends at the expert of tile q
+      before += te;
+      te = __builtin_amdgcn_readfirstlane(row_tiles(++walk));
+    }
     rows_of(expert_rows, walk, capacity, num_rows, first, count);
-    const uint32_t before = __builtin_amdgcn_readfirstlane(start[walk]);
-    const uint32_t te = __builtin_amdgcn_readfirstlane(start[walk + 1]) - before;
     const uint32_t local = tile - before * nt;
-    const int m0 = static_cast<int>(local % te) * BM;
-    once = te == 1;
+    m0 = static_cast<int>(local % te) * BM;
     n0 = static_cast<int>(local / te) * BO;
-    rows = __builtin_amdgcn_readfirstlane(min(count - m0, BM));  // >= 1
-    row0 = __builtin_amdgcn_readfirstlane(first) + m0;
-    const size_t we = static_cast<size_t>(walk) * N;
-    wr = make_rsrc(w + we * wrow_bytes, static_cast<uint32_t>(N) * wrow_bytes);
-    ar = make_rsrc(a + static_cast<size_t>(row0) * arow_bytes, static_cast<uint32_t>(rows) * arow_bytes);
-    wsr = make_rsrc(w_scale + we * srow_bytes, static_cast<uint32_t>(N) * srow_bytes);
-    asr = make_rsrc(a_scale + static_cast<size_t>(row0) * srow_bytes, static_cast<uint32_t>(rows) * srow_bytes);
-    const auto weight_row = [&](int r0, int r) -> uint32_t {  // r0: wave-uniform, of the same half as r
-      const uint32_t n = min(n0 + (GATED && r0 >= BO ? r - BO : r), O - 1);
-      return GATED && r0 >= BO ? n + O : n;
-    };
+    wr = make_rsrc(w + static_cast<size_t>(walk) * N * wrow_bytes, static_cast<uint32_t>(N) * wrow_bytes);
 #pragma unroll
     for (int i = 0; i < LW; ++i) {
       const int r0 = (i * NW + wave) * 8, r = r0 + (lane >> 3);
       woff[i] = weight_row(r0, r) * wrow_bytes + ((lane & 7) ^ swizzle8(r)) * 16;
     }
+  };
+  const auto open_rows = [&]() {
+    rows = __builtin_amdgcn_readfirstlane(min(count - m0, BM));  // >= 1
+    row0 = __builtin_amdgcn_readfirstlane(first) + m0;
+    ar = make_rsrc(a + static_cast<size_t>(row0) * arow_bytes, static_cast<uint32_t>(rows) * arow_bytes);
+    wsr = make_rsrc(w_scale + static_cast<size_t>(walk) * N * srow_bytes, static_cast<uint32_t>(N) * srow_bytes);
+    asr = make_rsrc(a_scale + static_cast<size_t>(row0) * srow_bytes, static_cast<uint32_t>(rows) * srow_bytes);
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
       const int r = (i * NW + wave) * (1024 / AB) + lane / (AB / 16);
       aoff[i] = min(r, rows - 1) * arow_bytes + (FP8 ? (lane & 15) ^ swizzle16(r) : (lane & 7) ^ swizzle8(r)) * 16;
     }
 #pragma unroll
-    for (int i = 0; i < LS; ++i) {
-      const int r0 = (i * NW + wave) * 32, r = r0 + (lane >> 1);
-      soff[i] = (r0 < BN ? weight_row(r0, r) : min(r - BN, rows - 1)) * srow_bytes;
+    for (int i = 0; i < LSW; ++i) {
+      const int r0 = (i * NW + wave) * (1024 / SW);
+      swoff[i] = weight_row(r0, r0 + lane / (SW / 16)) * srow_bytes;
     }
+#pragma unroll
+    for (int i = 0; i < LSA; ++i) saoff[i] = min((i * NW + wave) * 32 + (lane >> 1), rows - 1) * srow_bytes;
   };
-  // Part Q of 4 of a stage's copies.  In a last stage of 128 channels the
-  // pieces of the missing half are read past the end of the buffer resource
-  // (kNone), which gives zero codes.
-  const auto copy_part = [&](auto qc, int s, uint8_t* wb, uint8_t* ab) {
-    constexpr int Q = decltype(qc)::value;
+  // A stage's copies.  In a last stage of 128 channels the pieces of the
+  // missing half are read past the end of the buffer resource (kNone), which
+  // gives zero codes.
+  const auto copy_weights = [&](int i, int s, bool none, uint8_t* wb) {
+    const int r0 = (i * NW + wave) * 8;
+    uint32_t off = woff[i];
+    // (no branches here: they would hide from the compiler how many copies are under way)
+    const uint32_t cut = tail && s == stages - 1 ? 4 : 0;
+    off |= none || (((lane & 7) ^ swizzle8(r0 + (lane >> 3))) & cut) ? kNone : 0;
+    if constexpr (NT) copy16_once(wr, wb + r0 * 128, off, s * 128); else copy16(wr, wb + r0 * 128, off, s * 128);
+  };
+  const auto copy_rows = [&](int s, uint8_t* ab) {
     const bool cut = tail && s == stages - 1;
 #pragma unroll
-    for (int i = Q; i < LW; i += 4) {
-      const int r0 = (i * NW + wave) * 8;
-      uint32_t off = woff[i];
-      if (cut && (((lane & 7) ^ swizzle8(r0 + (lane >> 3))) & 4)) off = kNone;
-      if (once) copy16_once(wr, wb + r0 * 128, off, s * 128); else copy16(wr, wb + r0 * 128, off, s * 128);
-    }
-#pragma unroll
-    for (int i = Q; i < LA; i += 4) {
+    for (int i = 0; i < LA; ++i) {
       const int r0 = (i * NW + wave) * (1024 / AB), r = r0 + lane / (AB / 16);
       uint32_t off = aoff[i];
       if (cut && (FP8 ? ((lane & 15) ^ swizzle16(r)) & 8 : ((lane & 7) ^ swizzle8(r)) & 4)) off = kNone;
       if (r0 < rows) copy16(ar, ab + r0 * AB, off, s * AB);
     }
   };
-  const auto copy_stage = [&](int s, uint8_t* wb, uint8_t* ab) {
-    static_for<0, 4>([&](auto q) { copy_part(q, s, wb, ab); });
-  };
   // 16 bytes of scales from 512-channel group g on, or the row's last 16
   const auto scale_at = [&](uint32_t g) { return min(g * 16, srow_bytes - 16); };
+  // piece p of weight row r's SW bytes lies at
+  const auto scale_place = [](uint32_t r, uint32_t p) {
+    return r * SW + ((SW == 64 ? p ^ ((r >> 1) & 3) ^ ((r >> 3) & 1) : p) * 16);
+  };
   const auto copy_scales = [&](int quad) {
+    if (quad % NQ == 0) {
+#pragma unroll
+      for (int i = 0; i < LSW; ++i) {
+        const int r0 = (i * NW + wave) * (1024 / SW), r = r0 + lane / (SW / 16);
+        const uint32_t p = (scale_place(r, lane % (SW / 16)) - r * SW) / 16;  // (its own inverse)
+        copy16(wsr, scw + r0 * SW, swoff[i] + scale_at(quad * 2 + p), 0);
+      }
+    }
     const uint32_t at = scale_at(quad * 2 + (lane & 1));
 #pragma unroll
-    for (int i = 0; i < LS; ++i) {
+    for (int i = 0; i < LSA; ++i) {
       const int r0 = (i * NW + wave) * 32;
-      if (r0 < BN) copy16(wsr, sc + r0 * 32, soff[i] + at, 0);
-      else if (r0 < BN + rows) copy16(asr, sc + r0 * 32, soff[i] + at, 0);
+      if (r0 < BM && r0 < rows) copy16(asr, sca + r0 * 32, saoff[i] + at, 0);
     }
   };
 
@@ -304,30 +363,30 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tiled(
   f32x16 acc[FN][FM];
   uint32_t sw[FN][4], sa[FM][4];  // scales of a pair of stages: one 32-bit word per 128 channels
   const auto read_scales = [&](int pair) {
-    const auto read4 = [&](int r, uint32_t one, uint32_t(&v)[4]) {
-      if (pair * 4 + 4 <= H / 128) {
-        const u32x4 q = *reinterpret_cast<const u32x4*>(sc + ((pair & 1) * 16 + r * 32));
+    // A row that is no multiple of 512 channels ends inside a pair: its last 16
+    // bytes were copied, and the missing words, for zero codes, are a scale of 1.
+    const int skip = (pair * 16 - static_cast<int>(scale_at(pair))) / 4;
+    const auto read4 = [&](const u32x4 q, uint32_t one, uint32_t(&v)[4]) {
+      if (skip == 0) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) v[x] = q[x];
       } else {
-        // the row's last 16 bytes were copied: the missing words, for zero
-        // codes, are a scale of 1
-        const uint32_t off = pair * 16 - scale_at(pair);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          v[x] = pair * 4 + x < H / 128
-                     ? *reinterpret_cast<const uint32_t*>(sc + ((pair & 1) * 16 + off + r * 32 + x * 4)) : one;
+        const uint32_t q1 = q[1], q2 = q[2], q3 = q[3];
+        v[0] = skip == 1 ? q1 : (skip == 2 ? q2 : q3);
+        v[1] = skip == 1 ? q2 : (skip == 2 ? q3 : one);
+        v[2] = skip == 1 ? q3 : one;
+        v[3] = one;
       }
     };
 #pragma unroll
     for (int i = 0; i < FN; ++i) {
-      read4(weight_frag(i) + col, 0x7F7F7F7Fu, sw[i]);
+      read4(*reinterpret_cast<const u32x4*>(scw + scale_place(weight_frag(i) + col, pair % (2 * NQ))), 0x7F7F7F7Fu, sw[i]);
 #pragma unroll
       for (int x = 0; x < 4; ++x) sw[i][x] >>= 8 * half;
     }
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
-      read4(BN + row_frag(j) + col, FP8 ? 0x3F800000u : 0x7F7F7F7Fu, sa[j]);
+      read4(*reinterpret_cast<const u32x4*>(sca + ((row_frag(j) + col) * 32 + (pair & 1) * 16)), FP8 ? 0x3F800000u : 0x7F7F7F7Fu, sa[j]);
 #pragma unroll
       for (int x = 0; x < 4; ++x) sa[j][x] >>= FP8 ? 0 : 8 * half;
     }
@@ -356,7 +415,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tiled(
   constexpr int U = 4 * FM;
   const auto step_of = [](int u) { return FP8 ? u / (2 * FM) * 2 + u % 2 : u / FM; };
   const auto frag_of = [](int u) { return FP8 ? u / 2 % FM : u % FM; };
-  const auto multiply = [&](auto xc, const uint8_t* wb, const uint8_t* ab, auto&& copies) {
+  const auto multiply = [&](auto xc, const uint8_t* wb, const uint8_t* ab) {
     constexpr int X = decltype(xc)::value;  // first word of the stage's scales
     i32x8 wv[4][FN], av[U];
 #pragma unroll
@@ -386,7 +445,6 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tiled(
           wv[3][i] = weight_piece(3, i, wb);
         }
       }
-      if constexpr (u < 4 && u < U / 2) copies(uc);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < FN; ++i) {
@@ -411,76 +469,116 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tiled(
     });
   };
 
-  open_tile();
-  copy_scales(0);
-  copy_stage(0, w0, a0);
+  // A tile's stages, and none or more without products that make them a
+  // multiple of WR, so that each tile starts with the same buffers.
+  const int padded = (stages + WR - 1) / WR * WR;
+  const auto start_rows = [&]() {
+    open_rows();
+    copy_scales(0);
+    copy_rows(0, a0);
+  };
+  open_weights();
+  start_rows();
+#pragma unroll
+  for (int x = 0; x < WR - 1; ++x) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < LW; ++i) copy_weights(i, x, false, x == 0 ? w0 : w1);
+  }
   for (;;) {
     const int c_n0 = n0, c_rows = rows, c_row0 = row0;  // the tile being multiplied
-    bool last = false;
+    bool last = false, early = false;
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
       for (int j = 0; j < FM; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-    const bool mine = wm * 32 < c_rows;  // else this wave's rows are all past the end
-    // stage 4 * quad + X, in (wb, ab); the next one goes to (wnext, anext)
-    const auto stage = [&](int quad, auto xc, const uint8_t* wb, const uint8_t* ab, uint8_t* wnext, uint8_t* anext) {
-      constexpr int X = decltype(xc)::value;
-      const int st = quad * 4 + X;
-      int to = st + 1;  // the stage to copy
-      wait_and_sync();
-      if (X % 2 == 0) read_scales(quad * 2 + X / 2);
-      if (X == 3) {
-        // the next quad's scales, or the next tile's first
-        const bool end = quad + 1 == quads;
-        if (end) {
-          t += step;
-          last = t >= run || base + t >= tiles;
-          if (!last) open_tile();
-          to = last ? stages : 0;
-        }
-        if (!last) copy_scales(end ? 0 : quad + 1);
+    const bool live = wm * 32 < c_rows;  // else this wave's rows are all past the end
+    const auto stage = [&](int st, auto pc) {
+      constexpr int P = decltype(pc)::value, X = P % 4, PW = P % WR, PN = (P + WR - 1) % WR;
+      const uint8_t* wb = PW == 0 ? w0 : (PW == 1 ? w1 : w2);
+      uint8_t* wnext = PN == 0 ? w0 : (PN == 1 ? w1 : w2);
+      const uint8_t* ab = P % 2 == 0 ? a0 : a1;
+      uint8_t* anext = P % 2 == 0 ? a1 : a0;
+      // all has arrived but (WR 3) the next stage's weights, which were copied last
+      wait_and_sync<(WR - 2) * LW>();
+      if (X % 2 == 0 && st < stages) read_scales(st >> 1);
+      if (P % WR == 1 && st + WR - 1 == padded) {  // from here on the weights are the next tile's
+        tile += step;
+        last = tile >= end;
+        if (!last) open_weights();
       }
-      const auto copies = [&](auto q) {
-        if (to < stages) copy_part(q, to, wnext, anext);
-      };
-      if (mine && st < stages) {
-        multiply(std::integral_constant<int, X % 2 * 2>{}, wb, ab, copies);
-        static_for<(U / 2 < 4 ? U / 2 : 4), 4>(copies);
-      } else {
-        static_for<0, 4>(copies);
+      if (st + 1 < stages) {
+        if (X == 3) copy_scales((st >> 2) + 1);
+        copy_rows(st + 1, anext);
+      } else if (P % WR == WR - 1 && X % 2 == 1 && st + 1 == padded && !last) {  // nothing reads a0 and the scales now
+        early = true;
+        start_rows();
       }
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");  // the weights are the last ones: the wait above counts on it
+      int s = st + WR - 1;
+      bool none = s >= stages;
+      if (s >= padded) {
+        s -= padded;
+        none = last;
+      }
+#pragma unroll
+      for (int i = 0; i < LW; ++i) copy_weights(i, s, none, wnext);
+      __builtin_amdgcn_sched_barrier(0);
+      if (live && st < stages) multiply(std::integral_constant<int, X % 2 * 2>{}, wb, ab);
     };
-    for (int quad = 0; quad < quads; ++quad) {
-      stage(quad, std::integral_constant<int, 0>{}, w0, a0, w1, a1);
-      stage(quad, std::integral_constant<int, 1>{}, w1, a1, w0, a0);
-      stage(quad, std::integral_constant<int, 2>{}, w0, a0, w1, a1);
-      stage(quad, std::integral_constant<int, 3>{}, w1, a1, w0, a0);
-    }
+    constexpr int kRing = WR == 3 ? 12 : 4;  // stages after which buffers and scales repeat
+    // (leaving the loop inside a round, not passing over the stages left of it:
+    // the compiler follows the copies under way along every path)
+    for (int first = 0;; first += kRing)
+      if (!static_while<0, kRing>([&](auto pc) {
+            constexpr int P = decltype(pc)::value;
+            stage(first + P, pc);
+            return (P + 1) % WR != 0 || first + P + 1 < padded;
+          }))
+        break;
 
+    // y: a fragment's 32 rows of 32 channels go through LDS, so that four lanes
+    // store 64 bytes of a row (from the accumulators' layout it would be 16).
+    // a1 is free: nothing is copied there before the next tile's first barrier.
+    wait_reads();
+    uint8_t* const yb = a1 + wave * 2048;
+    // 16-byte piece p of the fragment's row r lies at
+    const auto y_place = [](uint32_t r, uint32_t p) { return r * 64 + (p ^ ((r >> 2) & 3)) * 16; };
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      const int m = row_frag(j) + col;
-      if (m >= c_rows) continue;
-      uint16_t* yrow = y + static_cast<size_t>(c_row0 + m) * O;
+    for (int j = 0; j < FM; ++j)
 #pragma unroll
-      for (int i = 0; i < (GATED ? FN / 2 : FN); ++i)
+      for (int i = 0; i < (GATED ? FN / 2 : FN); ++i) {
+        if (row_frag(j) >= c_rows) continue;
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
-          const int n = c_n0 + weight_frag(i) + 8 * r4 + 4 * half;
-          if (n >= O) continue;
           __bf16 o[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const float v = acc[i][j][4 * r4 + x];
             o[x] = static_cast<__bf16>(GATED ? silu_mul(v, acc[GATED ? i + FN / 2 : i][j][4 * r4 + x]) : v);
           }
-          *reinterpret_cast<uint2*>(yrow + n) = *reinterpret_cast<uint2*>(o);
+          *reinterpret_cast<uint2*>(yb + (y_place(col, r4) + half * 8)) = *reinterpret_cast<uint2*>(o);
         }
-    }
+        asm volatile("" ::: "memory");
+        const int n = c_n0 + weight_frag(i) + (lane & 3) * 8;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int r = x * 16 + (lane >> 2), m = row_frag(j) + r;
+          const u32x4 v = *reinterpret_cast<const u32x4*>(yb + y_place(r, lane & 3));
+          if (m < c_rows && n < O) *reinterpret_cast<u32x4*>(y + static_cast<size_t>(c_row0 + m) * O + n) = v;
+        }
+        asm volatile("" ::: "memory");
+      }
     if (last) break;
+    if (!early) {
+      start_rows();
+      __builtin_amdgcn_s_waitcnt(15 << 8 | 7 << 4);  // vmcnt(0): the first wait counts on the weights being last
+    }
   }
+  __builtin_amdgcn_s_waitcnt(15 << 8 | 7 << 4);  // vmcnt(0): no copy outlives the workgroup's LDS
 }
 
 }  // namespace
@@ -501,15 +599,33 @@ hipError_t launch_expert_product(const void* a, const void* a_scale, bool fp8, c
     constexpr bool F = decltype(f)::value, G = decltype(g)::value;
     // rows too short for 16-byte pieces of scales
     if (H < 512) return with(product_kernel<F, G>, 2048, kThreads);
+    // Tile by the mean rows of an expert (the padded layout tells nothing about
+    // them: as for few).  Few rows: the weights' stream decides, and small
+    // workgroups keep it up, two on a CU; many rows: tiles that reuse what they
+    // read, one workgroup on a CU.  Measured with E 256, H 7168, N 4096 gated,
+    // in microseconds, at tokens x 8 rows each:
+    //   MXFP4 rows      tokens    1   128  1024  2048  4096  8192  32768
+    //   64 x 128, 3 stages       28   576   688  1070
+    //   128 x 128                         765   845  1311
+    //   192 x 256                        1005   925   982  2009   5419
+    //   256 x 256                                    1140  1747   4642
+    //   FP8 rows        tokens    1   128  1024  2048  4096  8192
+    //   64 x 128                 43   620   768  1219
+    //   64 x 128, 3 stages       40   848 (one workgroup fits a CU)
+    //   128 x 256                         938  1060  1584  2575
+    // Weights of an expert with one row tile are read once and non-temporally
+    // (576 against 595 at 128 tokens); where more row tiles read them, that
+    // would keep them out of L2 (192 x 256 at 32768 tokens: 5419 against 4922).
     const int64_t avg = capacity > 0 ? 0 : num_rows / E;
     if constexpr (F) {
-      if (avg <= 16) return with(product_tiled<F, G, 64, 128, 2, 2>, 512, 256);
-      return with(product_tiled<F, G, 128, 256, 2, 4>, 256, 512);
+      if (avg <= 32) return with(product_tiled<F, G, 64, 128, 2, 2, 2, true>, 512, 256);
+      if (avg <= 128) return with(product_tiled<F, G, 128, 256, 2, 4, 2, true>, 256, 512);
+      return with(product_tiled<F, G, 128, 256, 2, 4, 2, false>, 256, 512);
     } else {
-      if (avg <= 16) return with(product_tiled<F, G, 32, 128, 1, 2>, 768, 128);
-      if (avg <= 64) return with(product_tiled<F, G, 128, 128, 2, 2>, 512, 256);
-      if (avg <= 170) return with(product_tiled<F, G, 192, 256, 2, 4>, 256, 512);
-      return with(product_tiled<F, G, 256, 256, 2, 4>, 256, 512);
+      if (avg <= 32) return with(product_tiled<F, G, 64, 128, 2, 2, 3, true>, 512, 256);
+      if (avg <= 64) return with(product_tiled<F, G, 128, 128, 2, 2, 2, true>, 512, 256);
+      if (avg <= 170) return with(product_tiled<F, G, 192, 256, 2, 4, 2, true>, 256, 512);
+      return with(product_tiled<F, G, 256, 256, 2, 4, 2, false>, 256, 512);
     }
   };
   if (fp8) return gated ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{});

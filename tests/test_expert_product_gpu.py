@@ -103,6 +103,16 @@ def test_product_large_rows(gpu, fmt, gated):
     run(gpu, [1, 2000], 7168, 32, fmt, gated)
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
+@pytest.mark.parametrize("H", [512, 640, 1280])
+@pytest.mark.parametrize("experts,rows,N", [(45, 5, 1536), (24, 50, 2816), (12, 130, 5888), (7, 300, 5120)])
+def test_product_stages(gpu, experts, rows, N, H, fmt):
+    """Rows of two, three and five stages, each tile, several tiles in turn on a workgroup."""
+    rng = np.random.default_rng(H)
+    counts = rng.integers(0, 2 * rows + 1, experts).tolist()
+    run(gpu, counts, H, N, fmt, H % 256 == 0 and N % 512 == 0, seed=H)
+
+
 def test_product_clamps_bad_spans(gpu):
     """Offsets and counts outside the buffer are clamped to it."""
     ep = gpu
