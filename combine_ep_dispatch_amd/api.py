@@ -125,6 +125,12 @@ def _device_of(first, *others):
     return _here if i == torch.cuda.current_device() else torch.cuda.device(i)
 
 
+def _dispatch_device(format, *tensors):
+    """_device_of for the MXFP4 rows; the other formats go to the current
+    device, as they always have."""
+    return _device_of(*tensors) if format == EP_RECV_MXFP4_G32 else _here
+
+
 def _ids_fn(name, topk_idx):
     """The C entry point for these ids: NAME, or NAME_i64 for int64 ids."""
     return getattr(LIB, name + "_i64") if topk_idx.dtype == torch.int64 else getattr(LIB, name)
@@ -220,11 +226,12 @@ def ep_dispatch(x, slot, topk_weights, format, recv_x, recv_scale=None, recv_wei
     _need_recv(format, recv_x, recv_scale, R, H)
     if recv_weight is not None:
         _need(recv_weight, "recv_weight", _F32, (R,))
-    check("ep_dispatch", LIB.ep_dispatch(
-        x.data_ptr(), T, H, K, slot.data_ptr(),
-        topk_weights.data_ptr() if topk_weights is not None else None, int(format), recv_x.data_ptr(),
-        recv_scale.data_ptr() if recv_scale is not None else None,
-        recv_weight.data_ptr() if recv_weight is not None else None, _stream(stream)))
+    with _dispatch_device(format, x, slot, topk_weights, recv_x, recv_scale, recv_weight):
+        check("ep_dispatch", LIB.ep_dispatch(
+            x.data_ptr(), T, H, K, slot.data_ptr(),
+            topk_weights.data_ptr() if topk_weights is not None else None, int(format), recv_x.data_ptr(),
+            recv_scale.data_ptr() if recv_scale is not None else None,
+            recv_weight.data_ptr() if recv_weight is not None else None, _stream(stream)))
 
 
 def _check_layout_dispatch(topk_idx, x, topk_weights, num_experts, capacity, format, tokens_per_expert,
@@ -272,12 +279,14 @@ def ep_layout_dispatch(topk_idx, x, topk_weights, num_experts, capacity, format,
     if workspace is not None:
         _need(workspace, "workspace", (torch.uint8, torch.int32))
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    check("ep_layout_dispatch", _ids_fn("ep_layout_dispatch", topk_idx)(
-        topk_idx.data_ptr(), x.data_ptr(), topk_weights.data_ptr() if topk_weights is not None else None, T, H, K,
-        E, cap, int(format), tokens_per_expert.data_ptr(),
-        expert_offset.data_ptr() if expert_offset is not None else None, slot.data_ptr(), src_token.data_ptr(),
-        recv_x.data_ptr(), recv_scale.data_ptr() if recv_scale is not None else None,
-        recv_weight.data_ptr() if recv_weight is not None else None, ws_ptr, ws_bytes, _stream(stream)))
+    with _dispatch_device(format, x, topk_idx, topk_weights, tokens_per_expert, expert_offset, slot, src_token, recv_x,
+                          recv_scale, recv_weight, workspace):
+        check("ep_layout_dispatch", _ids_fn("ep_layout_dispatch", topk_idx)(
+            topk_idx.data_ptr(), x.data_ptr(), topk_weights.data_ptr() if topk_weights is not None else None, T, H, K,
+            E, cap, int(format), tokens_per_expert.data_ptr(),
+            expert_offset.data_ptr() if expert_offset is not None else None, slot.data_ptr(), src_token.data_ptr(),
+            recv_x.data_ptr(), recv_scale.data_ptr() if recv_scale is not None else None,
+            recv_weight.data_ptr() if recv_weight is not None else None, ws_ptr, ws_bytes, _stream(stream)))
 
 
 def ep_layout_dispatch_noalloc(topk_idx, x, topk_weights, num_experts, capacity, format, tokens_per_expert,
@@ -291,12 +300,14 @@ def ep_layout_dispatch_noalloc(topk_idx, x, topk_weights, num_experts, capacity,
         raise TypeError("ep_layout_dispatch_noalloc takes int32 topk_idx")
     T, H, K = _check_layout_dispatch(topk_idx, x, topk_weights, num_experts, capacity, format, tokens_per_expert,
                                      expert_offset, slot, src_token, recv_x, recv_scale, recv_weight)
-    check("ep_layout_dispatch_noalloc", LIB.ep_layout_dispatch_noalloc(
-        topk_idx.data_ptr(), x.data_ptr(), topk_weights.data_ptr() if topk_weights is not None else None, T, H, K,
-        int(num_experts), int(capacity), int(format), tokens_per_expert.data_ptr(),
-        expert_offset.data_ptr() if expert_offset is not None else None, slot.data_ptr(), src_token.data_ptr(),
-        recv_x.data_ptr(), recv_scale.data_ptr() if recv_scale is not None else None,
-        recv_weight.data_ptr() if recv_weight is not None else None, _stream(stream)))
+    with _dispatch_device(format, x, topk_idx, topk_weights, tokens_per_expert, expert_offset, slot, src_token, recv_x,
+                          recv_scale, recv_weight):
+        check("ep_layout_dispatch_noalloc", LIB.ep_layout_dispatch_noalloc(
+            topk_idx.data_ptr(), x.data_ptr(), topk_weights.data_ptr() if topk_weights is not None else None, T, H, K,
+            int(num_experts), int(capacity), int(format), tokens_per_expert.data_ptr(),
+            expert_offset.data_ptr() if expert_offset is not None else None, slot.data_ptr(), src_token.data_ptr(),
+            recv_x.data_ptr(), recv_scale.data_ptr() if recv_scale is not None else None,
+            recv_weight.data_ptr() if recv_weight is not None else None, _stream(stream)))
 
 
 def ep_combine(y, slot, topk_weights, out, stream=None, num_rows=None):
@@ -676,7 +687,10 @@ def expert_product(a, a_scale, w, w_scale, handle, activation=EP_ACT_NONE, strea
     FP8.  Rows of no expert hold no defined values."""
     format = EP_RECV_MXFP4_G32 if a_scale.dtype == torch.uint8 else EP_RECV_FP8_E4M3_G128
     padded = isinstance(handle, PaddedHandle)
-    a2, s2 = a.reshape(-1, a.shape[-1]), a_scale.reshape(-1, a_scale.shape[-1])
+    for name, t in (("a", a), ("a_scale", a_scale), ("w", w)):
+        if t.dim() < 2 or not t.is_contiguous():  # (a copy made here would be on the current stream, not on ``stream``)
+            raise ValueError("%s must be contiguous rows" % name)
+    a2, s2 = a.view(-1, a.shape[-1]), a_scale.view(-1, a_scale.shape[-1])
     out = w.shape[1] // 2 if activation == EP_ACT_SWIGLU else w.shape[1]
     y = torch.empty((a2.shape[0], out), dtype=torch.bfloat16, device=a.device)
     ep_expert_product(a2, s2, format, w, w_scale, handle.recv_expert_count if padded else handle.expert_offset,

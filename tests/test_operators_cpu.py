@@ -228,3 +228,16 @@ def test_wrappers_refuse_host_tensors_and_wrong_types(lib):
                            torch.zeros(2, 16, 64, dtype=torch.uint8), torch.zeros(2, 16, 4, dtype=torch.uint8), h)
     with pytest.raises(ValueError, match="unknown receive format"):
         lib.dispatch(torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 2, dtype=torch.int32), None, 8, format=9)
+
+
+def test_expert_product_refuses_rows_with_gaps(lib):
+    """A copy of them would be made on another stream than the product's."""
+    h = lib.Handle(None, torch.zeros(3, dtype=torch.int32), None, None, 2)
+    a, s = torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(4, 8, dtype=torch.uint8)
+    w, ws = torch.zeros(2, 16, 64, dtype=torch.uint8), torch.zeros(2, 16, 4, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="a must be contiguous"):
+        lib.expert_product(a[:, :64], s[:, :4].contiguous(), w, ws, h)
+    with pytest.raises(ValueError, match="a_scale must be contiguous"):
+        lib.expert_product(a[:, :64].contiguous(), s[:, :4], w, ws, h)
+    with pytest.raises(ValueError, match="w must be contiguous"):
+        lib.expert_product(a[:, :64].contiguous(), s[:, :4].contiguous(), w.transpose(1, 2), ws, h)
