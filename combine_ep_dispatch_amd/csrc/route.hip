@@ -4,6 +4,14 @@
 //
 // The choice is defined on binary64 scores, the work is done in binary32: see
 // "the binary32 path" below.
+//
+// A wavefront takes two tokens up to 256 experts (one beyond), each lane
+// holding consecutive experts in registers: memory is read once, in order, and
+// the choice is vector work between lanes, which is what bounds it.  32768
+// tokens of 256 experts in BF16, sigmoid, 4 of 8 groups, top 8: 27.6 us
+// (17 MB in, 2 MB out: 3 us at the rate of a copy); wholly in binary64, with
+// one token a wavefront, it was 94.  128 tokens are as fast as the host calls
+// (11 us).
 
 #include <hip/hip_runtime.h>
 
@@ -547,6 +555,13 @@ __device__ __forceinline__ void store_grad(uint16_t* p, float v) {
   *p = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
 
+// A wavefront per token; a lane holds experts 64 apart, so that a row leaves in
+// whole runs, and picks the K entries' terms out of the other lanes in order of
+// k: an id that occurs twice is added up the same way every time, without
+// atomics.  Sums are binary32; a BF16 gradient is rounded once, as it is
+// stored.  Bounded by vector work and by its stores: 32768 tokens of 256
+// experts in binary32, sigmoid, top 8: 18 us for 34 MB written (6 us at the
+// rate of a fill).
 template <typename Z, int EPL>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     const float* __restrict__ grad_w, const Z* __restrict__ logits, const int32_t* __restrict__ ids, int32_t T,
