@@ -8,12 +8,13 @@
 // consecutive channels of one row.  FP8 rows go through it with a scale of 1
 // and 128 channels at a time, whose sums are scaled on the vector unit.
 //
-// With E 256, H 7168, N 4096 gated and 8 experts a token: 1 token 25 us, 128
-// tokens 565 us (MXFP4 rows; the weights at 7.0 TB/s), 682 us (FP8 rows; the
-// same weights, four instead of one LDS piece a row and step), 4096 tokens 1013
-// us (4.2 TB/s and 1.9 PFLOP/s: bounded by copies into LDS that end at each
-// stage's barrier; without products 846, without copied rows 724), 32768 tokens
-// 4633 us (3.3 PFLOP/s; the matrix unit reaches 6.1 on such operands alone).
+// With E 256, H 7168, N 4096 gated and 8 experts a token: 1 token 25 us; 128
+// tokens 565 us with MXFP4 rows (the weights at 7.0 TB/s), 620 to 700 with FP8
+// rows (twice their bytes in LDS); 4096 tokens 920 to 1120 us by the card (4.3
+// TB/s, 1.9 PFLOP/s), bounded by copies into LDS that end at each stage's
+// barrier (without products 846 of 1120, without the rows' copies as well
+// 724); 32768 tokens 4633 us (3.3 PFLOP/s; the matrix unit reaches 6.1 on such
+// operands alone).
 
 #include "ep_device.h"
 #include "ep_internal.h"
@@ -134,9 +135,10 @@ __global__ __launch_bounds__(kThreads) void product_kernel(const uint8_t* __rest
 // on over the end of a tile into the next one.  LDS rows are 128 bytes (FP8
 // rows 256) and hold their 16-byte pieces permuted (piece ^ swizzle(row)), so
 // that the 16 lanes served together meet different banks.  Scales are copied
-// 64 bytes a weight row (eight stages; 32 where the tile is largest, which has
-// no registers left: 4642 against 4951 us) and 32 bytes a token row (four) at
-// a time: short pieces of many rows are what a copy costs most.
+// 64 bytes a weight row (eight stages) and 32 bytes a token row (four) at a
+// time: short pieces of many rows are what a copy costs most.  It is 32 for
+// both in the largest tile, which has no registers left (4642 against 4951
+// us), and where three stages of 256 weight rows leave no LDS.
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __amdgpu_buffer_rsrc_t Rsrc;
@@ -211,7 +213,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void product_tiled(
   constexpr int LA = BM * AB / 1024 / NW;           // 1024 / AB token rows each
   static_assert(LW * 8 * NW == BN && LA * 1024 * NW == BM * AB && FM * 32 * WM == BM && FN * 32 * WN == BN, "tile");
   static_assert(!GATED || FN % 2 == 0, "a wave holds both halves of its channels");
-  constexpr int SW = BM > 192 ? 32 : 64;            // bytes of a weight row's scales copied at a time
+  constexpr int SW = BM > 192 || (WR == 3 && BN > 128) ? 32 : 64;  // bytes of a weight row's scales copied at a time
   constexpr int NQ = SW / 32;                       // quads of stages in SW bytes of a weight row's scales
   constexpr int LSW = BN * SW / 1024 / NW;          // copies per wave for those: 1024 / SW rows each
   constexpr int LSA = (BM / 32 + NW - 1) / NW;      // token rows' scales, a quad's (32 bytes): 32 rows each
@@ -602,29 +604,33 @@ hipError_t launch_expert_product(const void* a, const void* a_scale, bool fp8, c
     // Tile by the mean rows of an expert (the padded layout tells nothing about
     // them: as for few).  Few rows: the weights' stream decides, and small
     // workgroups keep it up, two on a CU; many rows: tiles that reuse what they
-    // read, one workgroup on a CU.  Measured with E 256, H 7168, N 4096 gated,
-    // in microseconds, at tokens x 8 rows each:
-    //   MXFP4 rows      tokens    1   128  1024  2048  4096  8192  32768
-    //   64 x 128, 3 stages       28   576   688  1070
-    //   128 x 128                         765   845  1311
-    //   192 x 256                        1005   925   982  2009   5419
-    //   256 x 256                                    1140  1747   4642
-    //   FP8 rows        tokens    1   128  1024  2048  4096  8192
-    //   64 x 128                 43   620   768  1219
-    //   64 x 128, 3 stages       40   848 (one workgroup fits a CU)
-    //   128 x 256                         938  1060  1584  2575
+    // read, one workgroup on a CU.  Measured with E 256, H 7168, N 4096 gated
+    // (down: 4096 tokens, H 2048, N 7168), in microseconds; x3: three stages of
+    // weights are kept, else two:
+    //   MXFP4 rows   tokens   1   128  1024  2048  4096  8192  32768  down
+    //   64 x 128 x3          28   576   688  1070
+    //   64 x 128             40   619   733
+    //   128 x 128                       765   845  1311                 704
+    //   192 x 256 x3                               1122               503
+    //   192 x 256                             925  1122  2009   5419  554
+    //   256 x 256                                  1140  1747   4642  598
+    //   FP8 rows     tokens   1   128   512  1024  2048  4096  8192   down
+    //   64 x 128             43   620   809   823  1243
+    //   64 x 128 x3          40   848 (one workgroup fits a CU)
+    //   64 x 256 x3               752   691   733  1086  1564  2562    767
+    //   128 x 256                      1022   957  1051  1602  2531    800
     // Weights of an expert with one row tile are read once and non-temporally
     // (576 against 595 at 128 tokens); where more row tiles read them, that
     // would keep them out of L2 (192 x 256 at 32768 tokens: 5419 against 4922).
     const int64_t avg = capacity > 0 ? 0 : num_rows / E;
     if constexpr (F) {
-      if (avg <= 32) return with(product_tiled<F, G, 64, 128, 2, 2, 2, true>, 512, 256);
-      if (avg <= 128) return with(product_tiled<F, G, 128, 256, 2, 4, 2, true>, 256, 512);
+      if (avg <= 8) return with(product_tiled<F, G, 64, 128, 2, 2, 2, true>, 512, 256);
+      if (avg <= 170) return with(product_tiled<F, G, 64, 256, 2, 4, 3, true>, 256, 512);
       return with(product_tiled<F, G, 128, 256, 2, 4, 2, false>, 256, 512);
     } else {
       if (avg <= 32) return with(product_tiled<F, G, 64, 128, 2, 2, 3, true>, 512, 256);
       if (avg <= 64) return with(product_tiled<F, G, 128, 128, 2, 2, 2, true>, 512, 256);
-      if (avg <= 170) return with(product_tiled<F, G, 192, 256, 2, 4, 2, true>, 256, 512);
+      if (avg <= 170) return with(product_tiled<F, G, 192, 256, 2, 4, 3, true>, 256, 512);
       return with(product_tiled<F, G, 256, 256, 2, 4, 2, false>, 256, 512);
     }
   };
