@@ -18,6 +18,7 @@
 
 #include "ep_device.h"
 #include "ep_internal.h"
+#include "expert_rows.h"
 #include "mx_device.h"
 
 namespace ep {
@@ -37,8 +38,7 @@ __device__ __forceinline__ void rows_of(const int32_t* __restrict__ expert_rows,
     first = e * capacity;
     count = min(max(expert_rows[e], 0), capacity);
   } else {
-    first = min(max(expert_rows[e], 0), num_rows);
-    count = max(min(expert_rows[e + 1], num_rows) - first, 0);
+    span_rows(expert_rows[e], expert_rows[e + 1], num_rows, first, count);
   }
 }
 

@@ -215,3 +215,83 @@ def test_product_refuses_mismatched_shapes(gpu):
         ep.expert_product(z(4, 64), z(4, 4), z(3, 16, 64), z(3, 16, 4), h)
     with pytest.raises(ValueError):
         ep.expert_product(z(4, 96), z(4, 6), z(2, 16, 96), z(2, 16, 6), h)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
+@pytest.mark.parametrize("H", [512, 896])
+def test_product_clamps_bad_spans_in_tiles(gpu, H, fmt):
+    """Offsets and counts outside the buffer, at sizes that go in tiles."""
+    ep = gpu
+    rng = np.random.default_rng(H)
+    q, s, a = rows_of(rng, 400, H, fmt)
+    wq, ws, w = rows_of(rng, 4 * 48, H, "mxfp4")
+    for er, cap, spans in [([-5, 100, 50, 100000, 7], 0, [(0, 100), (100, 0), (50, 350), (400, 0)]),
+                           ([2 ** 31 - 1, -2 ** 31, 3, 3, 3], 0, [(400, 0), (0, 3), (3, 0), (3, 0)]),
+                           ([999, -3, 100, 2 ** 31 - 1], 100, [(0, 100), (100, 0), (200, 100), (300, 100)])]:
+        out = torch.full((400, 48), SENT_BF16, dtype=torch.int16, device="cuda")
+        print("case spans", H, fmt, er, cap, flush=True)
+        ep.ep_expert_product(to_dev(q), to_dev(s), ep.EP_RECV_FP8_E4M3_G128 if fmt == "fp8" else ep.EP_RECV_MXFP4_G32,
+                             to_dev(wq).view(4, 48, H // 2), to_dev(ws).view(4, 48, H // 32),
+                             to_dev(np.array(er, dtype=np.int32)), cap, ep.EP_ACT_NONE, out)
+        torch.cuda.synchronize()
+        y, mag = ops.expert_product(a, w.reshape(4, 48, H), spans, False)
+        got = out.cpu().numpy().view(np.uint16)
+        if er[0] == -5:  # experts 0 and 2 share rows 50..99: one of the two writes last
+            got, y, mag = [np.delete(v, range(50, 100), 0) for v in (got, y, mag)]
+        check(got, y, mag, H, False)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
+@pytest.mark.parametrize("H", [640, 1024])
+def test_product_nan_stays_in_its_row_and_channel_in_tiles(gpu, H, fmt):
+    """A NaN scale (or FP8 code) makes its row's sums NaN, one of the weights'
+    its channel's, and no others."""
+    ep = gpu
+    rng = np.random.default_rng(H)
+    N = 96
+    q, s, _ = rows_of(rng, 70, H, fmt)
+    wq, ws, _ = rows_of(rng, N, H, "mxfp4")
+    if fmt == "fp8":
+        q[2, H - 3], q[40, 5] = 0x7F, 0xFF
+        a = ops.fp8_values(q, s)
+    else:
+        s[2, H // 32 - 1], s[40, 0] = 255, 255
+        a = ops.mxfp4_values(q, s)
+    ws[5, 1], ws[77, H // 32 - 1] = 255, 255
+    y, mag = ops.expert_product(a, ops.mxfp4_values(wq, ws)[None], [(0, 70)], False)
+    out = torch.empty(70, N, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_product(to_dev(q), to_dev(s), ep.EP_RECV_FP8_E4M3_G128 if fmt == "fp8" else ep.EP_RECV_MXFP4_G32,
+                         to_dev(wq)[None], to_dev(ws)[None], to_dev(np.array([0, 70], dtype=np.int32)), 0,
+                         ep.EP_ACT_NONE, out)
+    v = out.double().cpu().numpy()
+    nan = np.zeros((70, N), dtype=bool)
+    nan[[2, 40]], nan[:, [5, 77]] = True, True
+    assert np.array_equal(np.isnan(v), nan)
+    err = H * 2.0 ** -23 * mag
+    assert np.all((np.abs(v - y) <= err + 2.0 ** -8 * (np.abs(y) + err) + 2.0 ** -126)[~nan])
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
+def test_product_offsets_beyond_32_bits(gpu, fmt):
+    """Rows and weights that lie more than 2^32 bytes into their buffers."""
+    ep = gpu
+    rng = np.random.default_rng(3)
+    H, N, E, R, n = 32768, 272, 1000, 270000, 37
+    q, s, a = rows_of(rng, n, H, fmt)
+    wq, ws, w = rows_of(rng, N, H, "mxfp4")
+    row, scale = (H, H // 128) if fmt == "fp8" else (H // 2, H // 32)
+    dq = torch.zeros(R, row, dtype=torch.uint8, device="cuda")
+    ds = torch.zeros(R, scale, dtype=torch.float32 if fmt == "fp8" else torch.uint8, device="cuda")
+    dw = torch.zeros(E, N, H // 2, dtype=torch.uint8, device="cuda")
+    dws = torch.zeros(E, N, H // 32, dtype=torch.uint8, device="cuda")
+    assert dq.numel() > 2 ** 32 and dw.numel() > 2 ** 32
+    dq[R - n:], ds[R - n:], dw[E - 1], dws[E - 1] = to_dev(q), to_dev(s), to_dev(wq), to_dev(ws)
+    off = torch.full((E + 1,), R - n, dtype=torch.int32, device="cuda")
+    off[E] = R
+    out = torch.full((R, N), SENT_BF16, dtype=torch.int16, device="cuda")
+    ep.ep_expert_product(dq, ds, ep.EP_RECV_FP8_E4M3_G128 if fmt == "fp8" else ep.EP_RECV_MXFP4_G32, dw, dws, off, 0,
+                         ep.EP_ACT_NONE, out)
+    torch.cuda.synchronize()
+    y, mag = ops.expert_product(a, w[None], [(0, n)], False)
+    check(out[R - n:].cpu().numpy().view(np.uint16), y, mag, H, False)
+    assert bool((out[:R - n] == SENT_BF16).all())
