@@ -1,0 +1,31 @@
+"""ep_route and ep_route_backward over the range of their inputs: many
+experts, logits far apart, tiny and huge scores.  Ids must be equal to the
+oracle's, weights within the stated 2^-20."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import operators as ops
+from tests.test_route_gpu import check_route
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("E", [520, 1000, 1024])
+def test_softmax_sum_over_many_experts(gpu, E):
+    """Twenty-one terms of just under 2^-24 beside a 1: added to it one after
+    the other in binary32 they all vanish, while together they are 20 units of
+    its last place, enough to change a weight beyond 2^-20 and, with a bias,
+    the choice."""
+    z = torch.full((3, E), -60.0)
+    z[:, 0] = 0.0
+    for e in list(range(1, 16)) + [16, 32, 64, 128, 256, 512]:
+        z[:, e] = float(np.float32(np.log(2.0 ** -24 * (1 - 2.0 ** -5))))
+    ids, w = check_route(gpu, z, 1, score=ops.SOFTMAX, renormalize=False)
+    assert ids.tolist() == [[0]] * 3
+    bias = torch.full((E,), -5.0)
+    bias[0] = 0.0
+    bias[E - 1] = 1 - 18 * 2.0 ** -24
+    ids, w = check_route(gpu, z, 1, score=ops.SOFTMAX, renormalize=False, bias=bias)
+    assert ids.tolist() == [[E - 1]] * 3
