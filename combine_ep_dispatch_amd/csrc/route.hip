@@ -247,16 +247,29 @@ __device__ __attribute__((noinline)) void route_token(const Z* __restrict__ logi
 // matter lie nearer than their rounding errors, the token is done again by
 // route_token.
 
-// e^z within a few units of binary32's last place (0 where it leaves the
-// normal range): exp2 of z log2(e), whose rounding error is put back.
-__device__ __forceinline__ float exp32(float z) {
+// Errors below are relative, in units of 2^-24, at most; those of the helpers
+// were measured over every binary32 argument of their range.
+
+// e^(z + rest), |rest| <= 2^-17, 0 where it leaves the normal range: exp2 of
+// z log2(e), whose rounding error is put back with rest.  2.9 units.
+__device__ __forceinline__ float exp32(float z, float rest = 0.0f) {
   const float y = z * 0x1.715476p+0f;
   const float r = __builtin_fmaf(z, 0x1.4ae0bep-26f, __builtin_fmaf(z, 0x1.715476p+0f, -y));
   const float e = __builtin_amdgcn_exp2f(y);
-  return __builtin_fmaf(e * r, 0x1.62e430p-1f, e);
+  return __builtin_fmaf(e * __builtin_fmaf(rest, 0x1.715476p+0f, r), 0x1.62e430p-1f, e);
 }
 
-// 1 / (1 + e^-z), likewise.
+// e^(x - m), x <= m: the difference's rounding error, up to 2^-18 for logits
+// 64 to 128 apart, goes into the exponential with it.  2.9 units; 0 for x =
+// -inf and below e^-150.
+__device__ __forceinline__ float exp32_diff(float x, float m) {
+  const float d = x - m;
+  const float b = d - x;
+  const float rest = (x - (d - b)) + (-m - b);
+  return d > -150.0f ? exp32(d, rest) : 0.0f;
+}
+
+// 1 / (1 + e^-z).  4.3 units.
 __device__ __forceinline__ float sigmoid32(float z) {
   const float e = exp32(fmaxf(-fabsf(z), -150.0f));
   return (z >= 0.0f ? 1.0f : e) * __builtin_amdgcn_rcpf(1.0f + e);
@@ -358,12 +371,12 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const Z* __restrict__ l
     zmax = from_order(max(lanes_max<LPT>(order_bits(zmax)), 0x00800000u));
     double sum = 0.0;  // (in binary32 up to 21 additions would each be off by 2^-24 of the sum)
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) sum += exp32(fmaxf(z[j] - zmax, -150.0f));  // (0 for -inf)
+    for (int j = 0; j < EPL; ++j) sum += exp32_diff(z[j], zmax);  // (0 for -inf)
     sum = lanes_sum<LPT>(sum);
     inv = sum > 0.0 ? 1.0f / static_cast<float>(sum) : 0.0f;
   }
   const auto score_of = [&](float x) {
-    return softmax ? exp32(fmaxf(x - zmax, -150.0f)) * inv : sigmoid32(x);
+    return softmax ? exp32_diff(x, zmax) * inv : sigmoid32(x);
   };
   // (key, index from behind): largest first, ties to the lower index; 0: off
   uint64_t k[EPL];
@@ -456,8 +469,10 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const Z* __restrict__ l
     if (BIAS) mag = from_order(lanes_max<LPT>(order_bits(mag)));
     if (best != 0) {
       const float lo = from_order(~worst), hi = from_order(best);
-      // each score is off by at most 2^-21.6 of itself (2^-22 + 2^-24 with a
-      // bias), the rule's own rounding by half of 2^-40
+      // a score is off by at most 8.8 units of itself (softmax: its exponential,
+      // the sum's, and three roundings; sigmoid 4.3), a sum of two by one more,
+      // with a bias by 13 of mag in all (two additions to it, and their sum):
+      // 32 units part them; the rule's own rounding is half of 2^-40
       near = lo - hi <= (BIAS ? 0x1p-19f * mag : 0x1p-19f * fmaxf(lo, hi) + 0x1p-38f);
     }
     if (whole) {
@@ -502,7 +517,9 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const Z* __restrict__ l
                                              : __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0u));
     if (BIAS && i > 0 && m != 0 && before != 0) {
       const float hi = from_order(before), lo = from_order(m);
-      // a score is off by at most 2^-22, and by 2^-24 of its sum with the bias
+      // two scores of a token are off by at most 8.8 units together (softmax:
+      // of their sum, at most 1; sigmoid: 4.3 of each), and each by one more
+      // for the bias: 16 units part them
       tie = tie || hi - lo <= 0x1p-20f * fmaxf(1.0f, fmaxf(fabsf(hi), fabsf(lo)));
     }
     before = m;
@@ -527,12 +544,14 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const Z* __restrict__ l
     // s / sum s, each s divided by exp(min(largest chosen logit, 0)) first so
     // that very negative logits do not underflow together
     const float m = from_order(max(lanes_max<LPT>(order_bits(zk)), 0x00800000u));
+    // 6.4 units each (the exponential, 1 + e, the division), as many again in
+    // their sum, and three roundings: within 16
     if (id >= 0) {
-      q = exp32(fmaxf(softmax ? zk - m : fminf(zk, 0.0f) - fminf(m, 0.0f), -150.0f));
-      if (!softmax) q *= __builtin_amdgcn_rcpf(1.0f + exp32(fmaxf(-fabsf(zk), -150.0f)));
+      q = softmax ? exp32_diff(zk, m) : exp32_diff(fminf(zk, 0.0f), fminf(m, 0.0f));
+      if (!softmax) q /= 1.0f + exp32(fmaxf(-fabsf(zk), -150.0f));
     }
-    const float sum = lanes_sum<LPT>(q);
-    if (sum > 0.0f) q *= __builtin_amdgcn_rcpf(sum);
+    const float sum = static_cast<float>(lanes_sum<LPT>(static_cast<double>(q)));
+    if (sum > 0.0f) q /= sum;
   } else if (id >= 0) {
     q = score_of(zk);
   }

@@ -400,7 +400,8 @@ ep_status ep_combine_backward(const void* grad_out, const void* y, const int32_t
  *   topk_idx[k] = the expert, topk_weights[k] = scale * s / S, where S is
  *       the sum of the chosen s (renormalize) or 1.
  * The choice is that of binary64 scores.  Weights are binary32, within
- * 2^-20 of their value relatively (values below 2^-126 may come out as 0).
+ * 2^-20 of their value relatively where s / S is at least 2^-120 (smaller
+ * ones may come out as 0).
  * Where fewer than K experts are left, the entries behind them get id -1
  * (masked everywhere in this library) and weight 0.
  *

@@ -29,3 +29,18 @@ def test_softmax_sum_over_many_experts(gpu, E):
     bias[E - 1] = 1 - 18 * 2.0 ** -24
     ids, w = check_route(gpu, z, 1, score=ops.SOFTMAX, renormalize=False, bias=bias)
     assert ids.tolist() == [[E - 1]] * 3
+
+
+@pytest.mark.parametrize("spread", [20.0, 40.0, 80.0])
+@pytest.mark.parametrize("score", [ops.SOFTMAX, ops.SIGMOID])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_weights_of_logits_far_apart(gpu, spread, score, renorm):
+    """A difference of logits rounded to binary32 before its exponential would
+    be off by up to 2^-18 at 64 and more: four times what is stated.  Smallest
+    scores e^-80 / 2^10: above 2^-126."""
+    rng = np.random.default_rng(int(spread))
+    for T, E, K in [(300, 32, 32), (40, 256, 32), (9, 700, 32)]:
+        z = torch.from_numpy((-spread * rng.random((T, E))).astype(np.float32))
+        check_route(gpu, z, K, score=score, renormalize=renorm)
+        z = torch.from_numpy((spread * (rng.random((T, E)) - 0.5)).astype(np.float32))
+        check_route(gpu, z, K, score=score, renormalize=renorm, n_group=4, topk_group=3)
