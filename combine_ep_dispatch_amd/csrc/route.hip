@@ -574,6 +574,15 @@ __device__ __forceinline__ void store_grad(uint16_t* p, float v) {
   *p = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
 
+// e^(x - m) with the difference's rounding error, up to 2^-18, put back.
+__device__ __forceinline__ float exp_diff(float x, float m) {
+  const float d = x - m;
+  const float b = d - x;
+  const float rest = (x - (d - b)) + (-m - b);
+  const float e = expf(d);
+  return d > -150.0f ? __builtin_fmaf(e, rest, e) : 0.0f;
+}
+
 // A wavefront per token; a lane holds experts 64 apart, so that a row leaves in
 // whole runs, and picks the K entries' terms out of the other lanes in order of
 // k: an id that occurs twice is added up the same way every time, without
@@ -607,7 +616,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      p[j] = p[j] > kNegInf ? expf(p[j] - zmax) : 0.0f;
+      p[j] = p[j] > kNegInf ? exp_diff(p[j], zmax) : 0.0f;
       sum += p[j];
     }
     sum = wave_sum(sum);
@@ -620,10 +629,10 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     if (on) {
       if (score == 1) {
         const float e = expf(-fabsf(zk));
-        u = expf(fminf(zk, 0.0f) - fminf(m, 0.0f)) / (1.0f + e);
+        u = exp_diff(fminf(zk, 0.0f), fminf(m, 0.0f)) / (1.0f + e);
         rest = (zk > 0.0f ? e : 1.0f) / (1.0f + e);  // 1 - s
       } else {
-        u = expf(zk - m);
+        u = exp_diff(zk, m);
       }
     }
     const float sum = wave_sum(u);
@@ -636,7 +645,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
       d = scale * g * e / ((1.0f + e) * (1.0f + e));
     }
   } else {
-    const float pk = on ? expf(zk - zmax) * inv : 0.0f;
+    const float pk = on ? exp_diff(zk, zmax) * inv : 0.0f;
     d = scale * g;
     dsum = wave_sum(scale * g * pk);
   }

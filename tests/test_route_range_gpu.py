@@ -44,3 +44,24 @@ def test_weights_of_logits_far_apart(gpu, spread, score, renorm):
         check_route(gpu, z, K, score=score, renormalize=renorm)
         z = torch.from_numpy((spread * (rng.random((T, E)) - 0.5)).astype(np.float32))
         check_route(gpu, z, K, score=score, renormalize=renorm, n_group=4, topk_group=3)
+
+
+@pytest.mark.parametrize("score", [ops.SOFTMAX, ops.SIGMOID])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradients_of_logits_far_apart(gpu, score, renorm):
+    """In units of 2^-24 of the magnitudes that make up an element: an
+    exponential 2.4 (1.4 measured, and one), a share of the sum 8 (softmax) or
+    12 (renormalised, both sides and three divisions' and conversions'
+    roundings), the sum over the K entries 5, products 3, and twice for the
+    mean that is taken off: below 40."""
+    rng = np.random.default_rng(3)
+    for T, E, K in [(2000, 8, 6), (200, 256, 8), (30, 1000, 32)]:
+        z = (-85.0 * rng.random((T, E))).astype(np.float32)
+        ids = np.argsort(rng.random((T, E)), axis=1)[:, :K].astype(np.int32)
+        g = rng.standard_normal((T, K)).astype(np.float32)
+        print("case gradients", T, E, K, score, renorm, flush=True)
+        got = gpu.route_backward(torch.from_numpy(g).cuda(), torch.from_numpy(z).cuda(), torch.from_numpy(ids).cuda(),
+                                 score=score, renormalize=renorm, scale=2.5).double().cpu().numpy()
+        want, mag = ops.route_backward(g, z, ids, score, renorm, 2.5)
+        bad = ~(np.abs(got - want) <= 40 * 2.0 ** -24 * mag + 2.0 ** -126)
+        assert not bad.any(), (int(bad.sum()), got[bad][:4], want[bad][:4])
