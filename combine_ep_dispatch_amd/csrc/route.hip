@@ -104,6 +104,18 @@ __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
   return static_cast<uint64_t>(hi) << 32 | lo;
 }
 
+// A group's score: the sum of its two largest v, a >= b (b = -inf: of its only
+// one), to 40 binary places below the larger one's magnitude, so that sums
+// that are equal in exact arithmetic tie whatever the exponentials' last bits.
+__device__ __forceinline__ double group_score(double a, double b) {
+  const bool two = b > -__builtin_inf();
+  const double sum = two ? a + b : a, m = fmax(fabs(a), two ? fabs(b) : 0.0);
+  if (!(m < __builtin_inf())) return sum;
+  int e;
+  frexp(m, &e);  // 2^(e-1) <= m < 2^e
+  return ldexp(rint(ldexp(sum, 41 - e)), e - 41);
+}
+
 // One token in binary64, by a whole wavefront: the rule as it stands.  Lane l
 // holds experts l * EPL ..; v_lds: E doubles of the wavefront, sum_lds: room
 // for EP_MAX_GROUPS doubles.
@@ -159,7 +171,7 @@ __device__ __attribute__((noinline)) void route_token(const Z* __restrict__ logi
       b = fmax(fmax(b, ob), fmin(a, oa));
       a = fmax(a, oa);
     }
-    const double gs = a > ninf ? rint((b > ninf ? a + b : a) * 0x1p40) : ninf;
+    const double gs = a > ninf ? group_score(a, b) : ninf;
     if (g < A.n_group && (lane & (P - 1)) == 0) sum_lds[g] = gs;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     const double mine = lane < A.n_group ? sum_lds[lane] : ninf;
@@ -472,8 +484,9 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const Z* __restrict__ l
       // a score is off by at most 8.8 units of itself (softmax: its exponential,
       // the sum's, and three roundings; sigmoid 4.3), a sum of two by one more,
       // with a bias by 13 of mag in all (two additions to it, and their sum):
-      // 32 units part them; the rule's own rounding is half of 2^-40
-      near = lo - hi <= (BIAS ? 0x1p-19f * mag : 0x1p-19f * fmaxf(lo, hi) + 0x1p-38f);
+      // 32 units part them; the rule's own rounding is 2^-41.  Scores that
+      // leave the normal range are off by up to 2^-126.
+      near = lo - hi <= (BIAS ? 0x1p-19f * mag : 0x1p-19f * fmaxf(lo, hi) + 0x1p-120f);
     }
     if (whole) {
       if (!((kept >> (sub / lanes & 63)) & 1)) {

@@ -394,7 +394,8 @@ ep_status ep_combine_backward(const void* grad_out, const void* y, const int32_t
  *   v = s + bias                    (bias steers the choice only)
  *   with n_group > 1, group j holds experts j*E/n_group ..; its score is
  *       the sum of its two largest v (of its only one), rounded to a
- *       multiple of 2^-40; the topk_group best groups are kept
+ *       multiple of 2^(q-40) where the larger magnitude of the two lies in
+ *       [2^q, 2^(q+1)); the topk_group best groups are kept
  *   the K best experts of the kept groups are chosen, in descending order
  *       of v (of z where there is no bias); ties go to the lower index
  *   topk_idx[k] = the expert, topk_weights[k] = scale * s / S, where S is

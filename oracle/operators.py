@@ -52,6 +52,16 @@ def _ratio(z, ids, score):
     return u / np.where(total > 0, total, 1.0)
 
 
+def group_score(best):
+    """The sum of a group's one or two largest v, rounded to 40 binary places
+    below the larger magnitude."""
+    total, m = sum(best), max(abs(v) for v in best)
+    if m == 0 or np.isinf(m):
+        return total
+    q = 41 - int(np.frexp(m)[1])  # m = f * 2^e with 0.5 <= f < 1
+    return float(np.ldexp(np.rint(np.ldexp(total, q)), -q))
+
+
 def route(logits, top_k, bias=None, n_group=1, topk_group=1, score=SIGMOID, renormalize=True, scale=1.0):
     """-> (ids int32 [T, K], weights float64 [T, K]); one token at a time."""
     z = clean_logits(logits)
@@ -70,7 +80,7 @@ def route(logits, top_k, bias=None, n_group=1, topk_group=1, score=SIGMOID, reno
             for g in range(n_group):
                 best = sorted((float(v[e]) for e in range(g * n, g * n + n) if on[e]), reverse=True)[:2]
                 if best:
-                    rank.append((-np.rint(sum(best) * 2.0 ** 40), g))
+                    rank.append((-group_score(best), g))
             kept = {g for _, g in sorted(rank)[:topk_group]}
             on = on & np.array([e // n in kept for e in range(E)])
         key = v if bias is not None else z[t]

@@ -65,3 +65,34 @@ def test_gradients_of_logits_far_apart(gpu, score, renorm):
         want, mag = ops.route_backward(g, z, ids, score, renorm, 2.5)
         bad = ~(np.abs(got - want) <= 40 * 2.0 ** -24 * mag + 2.0 ** -126)
         assert not bad.any(), (int(bad.sum()), got[bad][:4], want[bad][:4])
+
+
+def test_groups_of_small_scores(gpu):
+    """The best groups are those of the largest sums however small these are:
+    among scores of e^-60 and e^-30 the latter are chosen."""
+    z = torch.full((2, 16), -60.0)
+    z[0, 8:] = -30.0
+    z[1, 8:] = -59.0
+    for score in (ops.SOFTMAX, ops.SIGMOID):
+        ids, _ = check_route(gpu, z, 2, n_group=2, topk_group=1, score=score)
+        assert ids.tolist() == [[8, 9], [8, 9]]
+    ids, _ = check_route(gpu, z, 2, n_group=2, topk_group=1, score=ops.SIGMOID, bias=torch.zeros(16))
+    assert ids.tolist() == [[8, 9], [8, 9]]
+    rng = np.random.default_rng(4)
+    for shift in (-25.0, -60.0, -86.0, -200.0, -700.0):
+        for T, E, groups in ((65, 64, 8), (33, 120, 5), (5, 1024, 32)):
+            z = torch.from_numpy((shift + 3 * rng.standard_normal((T, E))).astype(np.float32))
+            z[1] -= 60 * torch.from_numpy(rng.random(E).astype(np.float32))
+            check_route(gpu, z, 4, n_group=groups, topk_group=2, score=ops.SIGMOID)
+            z[2, : E // groups] = 0.0  # softmax: the others' scores are small
+            check_route(gpu, z, 4, n_group=groups, topk_group=2, score=ops.SOFTMAX)
+
+
+def test_group_sums_that_are_equal_tie(gpu):
+    """s(x) + s(-x) = 1 whatever x: the lower group."""
+    x = torch.from_numpy(np.random.default_rng(6).random((200, 1)).astype(np.float32)) * 8
+    y = torch.from_numpy(np.random.default_rng(7).random((200, 1)).astype(np.float32)) * 8
+    low = torch.full((200, 2), -50.0)
+    z = torch.cat([x, -x, low, -y, y, low], 1)
+    ids, _ = check_route(gpu, z, 2, n_group=2, topk_group=1)
+    assert np.array_equal(np.sort(ids, axis=1), np.broadcast_to([0, 1], (200, 2)))
