@@ -485,8 +485,10 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const Z* __restrict__ l
       // the sum's, and three roundings; sigmoid 4.3), a sum of two by one more,
       // with a bias by 13 of mag in all (two additions to it, and their sum):
       // 32 units part them; the rule's own rounding is 2^-41.  Scores that
-      // leave the normal range are off by up to 2^-126.
-      near = lo - hi <= (BIAS ? 0x1p-19f * mag : 0x1p-19f * fmaxf(lo, hi) + 0x1p-120f);
+      // leave the normal range are off by up to 2^-126; sums that leave it
+      // (huge biases) say nothing.
+      const float gap = lo - hi;
+      near = !(gap > (BIAS ? 0x1p-19f * mag : 0x1p-19f * fmaxf(lo, hi) + 0x1p-120f) && gap < __builtin_inff());
     }
     if (whole) {
       if (!((kept >> (sub / lanes & 63)) & 1)) {

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from oracle import operators as ops
-from tests.test_route_gpu import check_route
+from tests.test_route_gpu import check_route, logits_of
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +96,20 @@ def test_group_sums_that_are_equal_tie(gpu):
     z = torch.cat([x, -x, low, -y, y, low], 1)
     ids, _ = check_route(gpu, z, 2, n_group=2, topk_group=1)
     assert np.array_equal(np.sort(ids, axis=1), np.broadcast_to([0, 1], (200, 2)))
+
+
+def test_group_sums_beyond_binary32(gpu):
+    """Biases whose sums leave binary32's range, infinite ones among them."""
+    z = logits_of(40, 32, 8, False)
+    top = float(torch.finfo(torch.float32).max)
+    bias = torch.zeros(32)
+    for first, second in [((3.0e38, 2.0e38), (3.2e38, 3.1e38)), ((3.0e38, 1.0e38), (top, top)),
+                          ((-2.0e38, -3.0e38), (-2.0e38, -2.5e38)), ((3.0e38, 3.0e38), (np.inf, 0.0)),
+                          ((np.inf, 1.0), (np.inf, 2.0)), ((np.inf, np.inf), (np.inf, np.inf)), ((1e38, 1e38), (3e38, -1e38))]:
+        bias[:8], bias[8:16] = min(first + (0.0,)) - 1.0, min(second + (0.0,)) - 1.0
+        bias[[3, 6]], bias[[9, 12]] = torch.tensor(first), torch.tensor(second)
+        for score in (ops.SOFTMAX, ops.SIGMOID):
+            for kept in (1, 2, 3):
+                check_route(gpu, z, 4, n_group=4, topk_group=kept, score=score, bias=bias)
+            check_route(gpu, z, 4, n_group=16, topk_group=5, score=score, bias=bias)
+            check_route(gpu, z[:, :30].contiguous(), 4, n_group=10, topk_group=2, score=score, bias=bias[:30].contiguous())
