@@ -129,7 +129,6 @@ __device__ __attribute__((noinline)) void route_token(const Z* __restrict__ logi
   for (int j = 0; j < EPL; ++j) {
     const int e = e0 + j;
     z[j] = e < E ? clean_logit(load_logit(logits + static_cast<size_t>(t) * E + e)) : kNegInf;
-    if (A.bias != nullptr && e < E && !(A.bias[e] > kNegInf)) z[j] = kNegInf;
     zmax = fmaxf(zmax, z[j]);
   }
   double s[EPL], total = 0.0;
@@ -148,8 +147,9 @@ __device__ __attribute__((noinline)) void route_token(const Z* __restrict__ logi
   uint64_t key[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
-    const bool on = z[j] > kNegInf;
-    const double v = s[j] + (A.bias != nullptr && e0 + j < E ? static_cast<double>(A.bias[e0 + j]) : 0.0);
+    const float bias = A.bias != nullptr && e0 + j < E ? A.bias[e0 + j] : 0.0f;
+    const bool on = z[j] > kNegInf && bias > kNegInf;
+    const double v = s[j] + static_cast<double>(bias);
     key[j] = !on ? 0 : order_bits(A.bias != nullptr ? v : static_cast<double>(z[j]));
     if (e0 + j < E) v_lds[e0 + j] = on ? v : ninf;
   }
@@ -375,11 +375,10 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const Z* __restrict__ l
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     z[j] = clean_logit(z[j]);
-    if (BIAS && !(bias[j] > kNegInf)) z[j] = kNegInf;
     zmax = fmaxf(zmax, z[j]);
   }
   const bool softmax = A.score == 0;
-  if (softmax) {  // the sum over all experts that are on
+  if (softmax) {  // the sum over all experts, those that the bias switches off among them
     zmax = from_order(max(lanes_max<LPT>(order_bits(zmax)), 0x00800000u));
     double sum = 0.0;  // (in binary32 up to 21 additions would each be off by 2^-24 of the sum)
 #pragma unroll
@@ -395,7 +394,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const Z* __restrict__ l
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const float v = BIAS ? score_of(z[j]) + bias[j] : z[j];
-    k[j] = z[j] > kNegInf ? static_cast<uint64_t>(order_bits(v)) << 32 | static_cast<uint32_t>(EPL - 1 - j) : 0;
+    k[j] = z[j] > kNegInf && (!BIAS || bias[j] > kNegInf) ? static_cast<uint64_t>(order_bits(v)) << 32 | static_cast<uint32_t>(EPL - 1 - j) : 0;
   }
 
   // Groups of whole lanes, a power of two of them, have their two largest in

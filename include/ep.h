@@ -408,7 +408,9 @@ ep_status ep_combine_backward(const void* grad_out, const void* y, const int32_t
  *
  * logits       float32 or bf16 [T, E] (logits_dtype: ep_dtype), aligned to
  *              an element
- * bias         float32 [E] or NULL; -inf or NaN switches an expert off
+ * bias         float32 [E] or NULL; an expert of bias -inf or NaN is never
+ *              chosen (its score stays in softmax's sum: s, and so the
+ *              gradient, does not depend on the bias)
  * topk_idx     int32 [T, K] out;  topk_weights float32 [T, K] out
  * Requirements: 1 <= E <= EP_MAX_EXPERTS, 1 <= K <= min(E, EP_MAX_TOPK),
  * 1 <= topk_group <= n_group <= EP_MAX_GROUPS, E % n_group == 0, scale

@@ -66,10 +66,10 @@ def route(logits, top_k, bias=None, n_group=1, topk_group=1, score=SIGMOID, reno
     """-> (ids int32 [T, K], weights float64 [T, K]); one token at a time."""
     z = clean_logits(logits)
     T, E = z.shape
-    if bias is not None:
+    s = scores(z, score)
+    if bias is not None:  # (steers the choice only: s is the logits')
         b = np.asarray(bias, dtype=np.float64)
         z = np.where(np.isnan(b) | np.isneginf(b), -np.inf, z)
-    s = scores(z, score)
     ids = np.full((T, top_k), -1, dtype=np.int32)
     for t in range(T):
         v = s[t] + (b if bias is not None else 0.0)

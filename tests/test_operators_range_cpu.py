@@ -23,3 +23,12 @@ def test_groups_of_small_scores():
     assert ids.tolist() == [[8, 9]] and w.tolist() == [[0.5, 0.5]]
     ids, _ = ops.route(z, 2, n_group=2, topk_group=1, score=ops.SOFTMAX)
     assert ids.tolist() == [[8, 9]]
+
+
+def test_the_bias_leaves_the_scores_alone():
+    z = np.array([[5.0, 1.0, 0.0, -1.0]])
+    bias = np.array([-np.inf, 0.0, np.nan, 0.0])
+    ids, w = ops.route(z, 2, bias=bias, score=ops.SOFTMAX, renormalize=False)
+    assert ids.tolist() == [[1, 3]]
+    assert np.allclose(w, np.exp(z[:, [1, 3]]) / np.exp(z).sum(), rtol=1e-14)
+    assert np.allclose(w, ops.route_weights(z, ids, ops.SOFTMAX, False, 1.0), rtol=1e-14)

@@ -113,3 +113,20 @@ def test_group_sums_beyond_binary32(gpu):
                 check_route(gpu, z, 4, n_group=4, topk_group=kept, score=score, bias=bias)
             check_route(gpu, z, 4, n_group=16, topk_group=5, score=score, bias=bias)
             check_route(gpu, z[:, :30].contiguous(), 4, n_group=10, topk_group=2, score=score, bias=bias[:30].contiguous())
+
+
+@pytest.mark.parametrize("score", [ops.SOFTMAX, ops.SIGMOID])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_switched_off_by_the_bias(gpu, score, renorm):
+    """The bias steers the choice only: the weights are those of the logits
+    alone, which is what route_backward differentiates."""
+    for E, groups, kept in ((16, 1, 1), (256, 8, 4), (700, 1, 1)):
+        z = logits_of(50, E, E, False)
+        bias = torch.zeros(E)
+        bias[1::3] = -np.inf
+        bias[5] = float("nan")
+        z[:, 1] = 6.0  # off, and most of softmax's sum
+        ids, w = check_route(gpu, z, 4, n_group=groups, topk_group=kept, score=score, bias=bias, renormalize=renorm, scale=2.0)
+        want = ops.route_weights(z.double().numpy(), ids, score, renorm, 2.0)
+        assert np.all(np.abs(w - want) <= 2.0 ** -20 * want)
+        check_route(gpu, z, 4, n_group=groups, topk_group=kept, score=score, bias=torch.full((E,), -np.inf), renormalize=renorm)
