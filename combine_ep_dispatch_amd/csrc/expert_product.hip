@@ -64,6 +64,29 @@ __device__ __forceinline__ void split_codes(i32x8 x, i32x8& low, i32x8& high) {
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
 
+// start[0 .. E] to the sums before each, by the workgroup's first wavefront;
+// every thread must call it.
+__device__ __forceinline__ void tiles_before(RowTiles* start, int E) {
+  if (threadIdx.x < kWave) {
+    const int per = E / kWave + 1, beg = threadIdx.x * per, end = min(beg + per, E + 1);
+    RowTiles mine = 0;
+    for (int e = beg; e < end; ++e) mine += start[e];
+    RowTiles run = mine;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const RowTiles o = __shfl_up(run, d);
+      if (static_cast<int>(threadIdx.x) >= d) run += o;
+    }
+    run -= mine;
+    for (int e = beg; e < end; ++e) {
+      const RowTiles n = start[e];
+      start[e] = run;
+      run += n;
+    }
+  }
+  __syncthreads();
+}
+
 template <bool FP8, bool GATED>
 __global__ __launch_bounds__(kThreads) void product_kernel(const uint8_t* __restrict__ a,
                                                            const uint8_t* __restrict__ a_scale,
@@ -73,7 +96,7 @@ __global__ __launch_bounds__(kThreads) void product_kernel(const uint8_t* __rest
                                                            int32_t E, int32_t capacity, int32_t H, int32_t N,
                                                            uint16_t* __restrict__ y) {
   constexpr int BM = 16, BN = 64;
-  __shared__ int start[kMaxExperts + 1];  // row tiles before each expert
+  __shared__ RowTiles start[kMaxExperts + 1];  // row tiles before each expert
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   for (int e = tid; e < E; e += kThreads) {
     int first, count;
@@ -82,28 +105,23 @@ __global__ __launch_bounds__(kThreads) void product_kernel(const uint8_t* __rest
   }
   if (tid == 0) start[E] = 0;
   __syncthreads();
-  block_exclusive_scan(start, E + 1);
+  tiles_before(start, E);
   const int O = GATED ? N / 2 : N;  // channels of y
   const int nt = (O + BN - 1) / BN;
-  const int64_t tiles = static_cast<int64_t>(start[E]) * nt;
+  const int64_t tiles = start[E] * nt;
   const int grp = lane >> 4, col = lane & 15;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int q = static_cast<int>(tile / nt);
-    int lo = 0, hi = E;  // the expert with start[lo] <= q < start[lo + 1]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (start[mid] <= q) lo = mid; else hi = mid;
-    }
+    const int e = expert_of_tile(start, E, tile / nt);
     int first, count;
-    rows_of(expert_rows, lo, capacity, num_rows, first, count);
-    const int te = start[lo + 1] - start[lo];
-    const int64_t local = tile - static_cast<int64_t>(start[lo]) * nt;
+    rows_of(expert_rows, e, capacity, num_rows, first, count);
+    const int64_t te = start[e + 1] - start[e];
+    const int64_t local = tile - start[e] * nt;
     const int m0 = static_cast<int>(local % te) * BM, n0 = static_cast<int>(local / te) * BN + wave * 16;
     const int m = m0 + col;
     const size_t row = static_cast<size_t>(first) + min(m, count - 1);
     const uint8_t* ap = a + row * (FP8 ? H : H / 2);
     const uint8_t* as = a_scale + row * (H / 32);
-    const size_t wrow = static_cast<size_t>(lo) * N + min(n0 + col, O - 1);
+    const size_t wrow = static_cast<size_t>(e) * N + min(n0 + col, O - 1);
     f32x4 acc[GATED ? 2 : 1];
 #pragma unroll
     for (auto& c : acc) c = f32x4{0, 0, 0, 0};

@@ -22,4 +22,19 @@ EP_ROWS_FN void span_rows(int32_t begin, int32_t end, int32_t num_rows, int32_t&
   count = last - first;
 }
 
+// A number of row tiles.  Wild offsets may span the whole buffer for every
+// other expert: 512 times 2^27 rows in tiles of 16 are 2^32.
+typedef int64_t RowTiles;
+
+// The expert whose row tiles start[e] .. start[e + 1] - 1 hold tile q <
+// start[E] (start: of E + 1, not falling, from 0 on).
+EP_ROWS_FN int expert_of_tile(const RowTiles* start, int E, RowTiles q) {
+  int lo = 0, hi = E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= q) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
 }  // namespace ep
