@@ -2,8 +2,9 @@
 
 Each ``ep_*`` function checks dtypes, devices, shapes and contiguity (the C
 side trusts buffer sizes), then passes raw device pointers and the current
-HIP stream to libep.so.  Every step of the computation runs in the
-library's kernels; torch only owns the memory and the stream.
+HIP stream of the operands' device to libep.so.  Every step of the
+computation runs in the library's kernels; torch only owns the memory and the
+stream.
 
 ``dispatch`` / ``combine`` mirror the pages' call shape
 ``dispatch(x, topk_idx, topk_weights, num_experts)`` returning received rows
@@ -11,7 +12,6 @@ and a handle, and ``combine(...)`` reducing back ([P4] "使用示例 › MoE 训
 的应用"; [P5] "典型工作流程").
 """
 
-import contextlib
 import os
 from collections import namedtuple
 
@@ -25,13 +25,16 @@ Handle = namedtuple("Handle", "tokens_per_expert expert_offset slot src_token nu
 PaddedHandle = namedtuple("PaddedHandle", "recv_expert_count slot src_token num_experts capacity")
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object: a few us less per call
+# without a Stream object, and without the check that the GPU is initialised
+# (the operands lie on it): a few us less per call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -112,7 +115,18 @@ def _format(fp8, format):
     return EP_RECV_FP8_E4M3_G128 if fp8 else EP_RECV_BF16
 
 
-_here = contextlib.nullcontext()
+class _Here:
+    """Leaves the current device as it is."""
+    __slots__ = ()
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, kind, value, trace):
+        pass
+
+
+_here = _Here()
 
 
 def _device_of(first, *others):
@@ -122,13 +136,18 @@ def _device_of(first, *others):
     for t in others:
         if t is not None and t.get_device() != i:
             raise ValueError("operands on different devices: %s and %s" % (first.device, t.device))
-    return _here if i == torch.cuda.current_device() else torch.cuda.device(i)
+    return _here if i == _current_device() else torch.cuda.device(i)
 
 
-def _dispatch_device(format, *tensors):
-    """_device_of for the MXFP4 rows; the other formats go to the current
-    device, as they always have."""
-    return _device_of(*tensors) if format == EP_RECV_MXFP4_G32 else _here
+def _transport_device(first, *others):
+    """_device_of for layouts, dispatch and combine, whose rows may lie in a
+    peer's memory: operands on several devices are launched from the current
+    one."""
+    i = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != i:
+            return _here
+    return _here if i == _current_device() else torch.cuda.device(i)
 
 
 def _ids_fn(name, topk_idx):
@@ -172,9 +191,10 @@ def ep_dispatch_layout(topk_idx, num_experts, tokens_per_expert, expert_offset, 
     if workspace is not None:
         _need(workspace, "workspace", (torch.uint8, torch.int32))
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    check("ep_dispatch_layout", _ids_fn("ep_dispatch_layout", topk_idx)(
-        topk_idx.data_ptr(), T, K, E, tokens_per_expert.data_ptr(), expert_offset.data_ptr(),
-        slot.data_ptr(), src_token.data_ptr(), ws_ptr, ws_bytes, _stream(stream)))
+    with _transport_device(topk_idx, tokens_per_expert, expert_offset, slot, src_token, workspace):
+        check("ep_dispatch_layout", _ids_fn("ep_dispatch_layout", topk_idx)(
+            topk_idx.data_ptr(), T, K, E, tokens_per_expert.data_ptr(), expert_offset.data_ptr(),
+            slot.data_ptr(), src_token.data_ptr(), ws_ptr, ws_bytes, _stream(stream)))
 
 
 def ep_dispatch_layout_padded(topk_idx, num_experts, capacity, recv_expert_count, slot, src_token,
@@ -196,9 +216,10 @@ def ep_dispatch_layout_padded(topk_idx, num_experts, capacity, recv_expert_count
     if workspace is not None:
         _need(workspace, "workspace", (torch.uint8, torch.int32))
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    check("ep_dispatch_layout_padded", _ids_fn("ep_dispatch_layout_padded", topk_idx)(
-        topk_idx.data_ptr(), T, K, E, cap, recv_expert_count.data_ptr(), slot.data_ptr(), src_token.data_ptr(),
-        ws_ptr, ws_bytes, _stream(stream)))
+    with _transport_device(topk_idx, recv_expert_count, slot, src_token, workspace):
+        check("ep_dispatch_layout_padded", _ids_fn("ep_dispatch_layout_padded", topk_idx)(
+            topk_idx.data_ptr(), T, K, E, cap, recv_expert_count.data_ptr(), slot.data_ptr(), src_token.data_ptr(),
+            ws_ptr, ws_bytes, _stream(stream)))
 
 
 def ep_dispatch(x, slot, topk_weights, format, recv_x, recv_scale=None, recv_weight=None, stream=None,
@@ -226,7 +247,7 @@ def ep_dispatch(x, slot, topk_weights, format, recv_x, recv_scale=None, recv_wei
     _need_recv(format, recv_x, recv_scale, R, H)
     if recv_weight is not None:
         _need(recv_weight, "recv_weight", _F32, (R,))
-    with _dispatch_device(format, x, slot, topk_weights, recv_x, recv_scale, recv_weight):
+    with _transport_device(x, slot, topk_weights, recv_x, recv_scale, recv_weight):
         check("ep_dispatch", LIB.ep_dispatch(
             x.data_ptr(), T, H, K, slot.data_ptr(),
             topk_weights.data_ptr() if topk_weights is not None else None, int(format), recv_x.data_ptr(),
@@ -279,8 +300,8 @@ def ep_layout_dispatch(topk_idx, x, topk_weights, num_experts, capacity, format,
     if workspace is not None:
         _need(workspace, "workspace", (torch.uint8, torch.int32))
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    with _dispatch_device(format, x, topk_idx, topk_weights, tokens_per_expert, expert_offset, slot, src_token, recv_x,
-                          recv_scale, recv_weight, workspace):
+    with _transport_device(x, topk_idx, topk_weights, tokens_per_expert, expert_offset, slot, src_token,
+                           recv_x, recv_scale, recv_weight, workspace):
         check("ep_layout_dispatch", _ids_fn("ep_layout_dispatch", topk_idx)(
             topk_idx.data_ptr(), x.data_ptr(), topk_weights.data_ptr() if topk_weights is not None else None, T, H, K,
             E, cap, int(format), tokens_per_expert.data_ptr(),
@@ -300,8 +321,8 @@ def ep_layout_dispatch_noalloc(topk_idx, x, topk_weights, num_experts, capacity,
         raise TypeError("ep_layout_dispatch_noalloc takes int32 topk_idx")
     T, H, K = _check_layout_dispatch(topk_idx, x, topk_weights, num_experts, capacity, format, tokens_per_expert,
                                      expert_offset, slot, src_token, recv_x, recv_scale, recv_weight)
-    with _dispatch_device(format, x, topk_idx, topk_weights, tokens_per_expert, expert_offset, slot, src_token, recv_x,
-                          recv_scale, recv_weight):
+    with _transport_device(x, topk_idx, topk_weights, tokens_per_expert, expert_offset, slot, src_token,
+                           recv_x, recv_scale, recv_weight):
         check("ep_layout_dispatch_noalloc", LIB.ep_layout_dispatch_noalloc(
             topk_idx.data_ptr(), x.data_ptr(), topk_weights.data_ptr() if topk_weights is not None else None, T, H, K,
             int(num_experts), int(capacity), int(format), tokens_per_expert.data_ptr(),
@@ -326,8 +347,9 @@ def ep_combine(y, slot, topk_weights, out, stream=None, num_rows=None):
     H = y.shape[1]
     _need(topk_weights, "topk_weights", _F32, (T, K))
     _need(out, "out", _BF16, (T, H))
-    check("ep_combine", LIB.ep_combine(y.data_ptr(), slot.data_ptr(), topk_weights.data_ptr(), T, H, K,
-                                       out.data_ptr(), _stream(stream)))
+    with _transport_device(y, slot, topk_weights, out):
+        check("ep_combine", LIB.ep_combine(y.data_ptr(), slot.data_ptr(), topk_weights.data_ptr(), T, H, K,
+                                           out.data_ptr(), _stream(stream)))
 
 
 def ep_dispatch_backward(grad_recv, slot, grad_x, stream=None, num_rows=None):
@@ -342,8 +364,9 @@ def ep_dispatch_backward(grad_recv, slot, grad_x, stream=None, num_rows=None):
         raise ValueError("grad_recv must be [%d, H]" % R)
     H = grad_recv.shape[1]
     _need(grad_x, "grad_x", _BF16, (T, H))
-    check("ep_dispatch_backward", LIB.ep_dispatch_backward(grad_recv.data_ptr(), slot.data_ptr(), T, H, K,
-                                                           grad_x.data_ptr(), _stream(stream)))
+    with _transport_device(grad_recv, slot, grad_x):
+        check("ep_dispatch_backward", LIB.ep_dispatch_backward(grad_recv.data_ptr(), slot.data_ptr(), T, H, K,
+                                                               grad_x.data_ptr(), _stream(stream)))
 
 
 def ep_combine_backward(grad_out, y, slot, topk_weights, grad_y, grad_w=None, stream=None, num_rows=None):
@@ -363,9 +386,10 @@ def ep_combine_backward(grad_out, y, slot, topk_weights, grad_y, grad_w=None, st
     if grad_w is not None:
         _need(y, "y", _BF16, (R, H))
         _need(grad_w, "grad_w", _F32, (T, K))
-    check("ep_combine_backward", LIB.ep_combine_backward(
-        grad_out.data_ptr(), y.data_ptr() if y is not None else None, slot.data_ptr(), topk_weights.data_ptr(),
-        T, H, K, grad_y.data_ptr(), grad_w.data_ptr() if grad_w is not None else None, _stream(stream)))
+    with _transport_device(grad_out, y if grad_w is not None else None, slot, topk_weights, grad_y, grad_w):
+        check("ep_combine_backward", LIB.ep_combine_backward(
+            grad_out.data_ptr(), y.data_ptr() if y is not None else None, slot.data_ptr(), topk_weights.data_ptr(),
+            T, H, K, grad_y.data_ptr(), grad_w.data_ptr() if grad_w is not None else None, _stream(stream)))
 
 
 def _logits_dtype(logits):
@@ -491,8 +515,9 @@ def ep_cast_fp8_e4m3(inp, out, stream=None):
     same shape."""
     _need(inp, "in", _F32)
     _need(out, "out", _U8, tuple(inp.shape))
-    check("ep_cast_fp8_e4m3", LIB.ep_cast_fp8_e4m3(inp.data_ptr(), out.data_ptr(), inp.numel(),
-                                                   _stream(stream)))
+    with _device_of(inp, out):
+        check("ep_cast_fp8_e4m3", LIB.ep_cast_fp8_e4m3(inp.data_ptr(), out.data_ptr(), inp.numel(),
+                                                       _stream(stream)))
 
 
 # ---- convenience wrappers that allocate their outputs ----------------------
