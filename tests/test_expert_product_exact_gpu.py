@@ -97,3 +97,23 @@ def test_exact_sums(gpu, H, gated, fmt):
 @pytest.mark.parametrize("H,every", [(7168, 64), (32768, 512)])
 def test_exact_long_sums(gpu, H, every, counts, gated, fmt):
     run(gpu, counts, H, 80, fmt, gated, every=every)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("H", [512, 640, 1024, 1280, 1536, 1792, 3328, 7168])
+@pytest.mark.parametrize("experts,rows,N", [(45, 5, 2048), (24, 50, 3328), (12, 130, 5888), (7, 400, 7168)])
+def test_exact_sums_over_several_tiles(gpu, experts, rows, N, H, gated, fmt):
+    """Every kernel of each format, with and without the activation, on more
+    tiles than workgroups: copies that run on into the next tile, after 2, 3,
+    4, 5, 6, 7, 13 and 28 stages, the last one half in some."""
+    counts = np.random.default_rng(experts + H).integers(0, 2 * rows + 1, experts).tolist()
+    run(gpu, counts, H, N, fmt, gated, every=8 if H < 1200 else 64, seed=rows)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("counts,capacity", [([7, 0, 96, 33], 96), ([300, 1, 257, 0, 64], 300)])
+@pytest.mark.parametrize("H", [256, 1024])
+def test_exact_sums_padded(gpu, counts, capacity, H, gated, fmt):
+    run(gpu, counts, H, 1040, fmt, gated, capacity=capacity)
