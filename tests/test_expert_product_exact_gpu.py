@@ -117,3 +117,54 @@ def test_exact_sums_over_several_tiles(gpu, experts, rows, N, H, gated, fmt):
 @pytest.mark.parametrize("H", [256, 1024])
 def test_exact_sums_padded(gpu, counts, capacity, H, gated, fmt):
     run(gpu, counts, H, 1040, fmt, gated, capacity=capacity)
+
+
+@pytest.mark.parametrize("counts", [[40], [9, 0, 15, 20], [400]], ids=["kernel", "few", "many"])
+@pytest.mark.parametrize("H", [128, 384, 512, 896, 2048])
+def test_every_fp8_code(gpu, counts, H):
+    """All finite codes side by side.  Not exact: 128
+    channels are at most 4 matrix instructions of 8 additions, then a scaled
+    addition to the sum so far, so (33 + H / 128) 2^-24 of the magnitudes, and
+    half a step of BF16."""
+    ep, N, E = gpu, 96, len(counts)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(H)
+    rows = sum(counts)
+    q = torch.randint(0, 256, (rows, H), generator=g, device="cuda", dtype=torch.uint8)
+    q = torch.where((q & 0x7F) == 0x7F, q ^ 1, q)
+    s = torch.rand(rows, H // 128, generator=g, device="cuda") + 0.5
+    wq, ws, wv, _ = codes4(g, E * N, H, 124, 130)
+    av = (q.view(torch.float8_e4m3fn).double().view(rows, -1, 128) * s.double().unsqueeze(-1)).view(rows, H)
+    first = np.concatenate([[0], np.cumsum(counts)]).tolist()
+    y = torch.empty(rows, N, dtype=torch.bfloat16, device="cuda")
+    print("case every code", counts, H, flush=True)
+    ep.ep_expert_product(q, s, ep.EP_RECV_FP8_E4M3_G128, wq.view(E, N, -1), ws.view(E, N, -1),
+                         torch.tensor(first, dtype=torch.int32, device="cuda"), 0, ep.EP_ACT_NONE, y)
+    for e, n in enumerate(counts):
+        r, wt = slice(first[e], first[e] + n), wv.view(E, N, H)[e].t().contiguous()
+        p, m = av[r] @ wt, av[r].abs() @ wt.abs()
+        err = (33 + H / 128) * 2.0 ** -24 * m
+        assert bool(((y[r].double() - p).abs() <= err + 2.0 ** -8 * (p.abs() + err)).all())
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8"])
+def test_largest_matrix(gpu, fmt):
+    """65536 channels in and out: 2^31 bytes of one expert's weights, of which
+    a few rows are not zero."""
+    ep, H, N, n, at = gpu, 65536, 65536, 5, [0, 1, 4095, 32767, 32768, 65400, 65535]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    a, s, av, unit_a = codes8(g, n, H, 1024) if fmt == "fp8" else codes4(g, n, H, 127, 128)
+    wq, ws, wv, unit_w = codes4(g, len(at), H, 120, 120)
+    w = torch.zeros(1, N, H // 2, dtype=torch.uint8, device="cuda")
+    scale = torch.full((1, N, H // 32), 127, dtype=torch.uint8, device="cuda")
+    w[0, at], scale[0, at] = wq, ws
+    y = torch.empty(n, N, dtype=torch.bfloat16, device="cuda")
+    print("case largest matrix", fmt, flush=True)
+    ep.ep_expert_product(a, s, ep.EP_RECV_FP8_E4M3_G128 if fmt == "fp8" else ep.EP_RECV_MXFP4_G32, w, scale,
+                         torch.tensor([0, n], dtype=torch.int32, device="cuda"), 0, ep.EP_ACT_NONE, y)
+    torch.cuda.synchronize()
+    assert float((av.abs() @ wv.abs().t().contiguous()).max()) < 2.0 ** 24 * unit_a * unit_w
+    want = torch.zeros(n, N, dtype=torch.bfloat16, device="cuda")
+    want[:, at] = (av @ wv.t().contiguous()).float().bfloat16()
+    assert torch.equal(y, want)
