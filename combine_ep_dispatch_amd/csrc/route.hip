@@ -8,9 +8,9 @@
 // A wavefront takes two tokens up to 256 experts (one beyond), each lane
 // holding consecutive experts in registers: memory is read once, in order, and
 // the choice is vector work between lanes, which is what bounds it.  32768
-// tokens of 256 experts in BF16, sigmoid, 4 of 8 groups, top 8: 27.6 us
-// (17 MB in, 2 MB out: 3 us at the rate of a copy); wholly in binary64, with
-// one token a wavefront, it was 94.  128 tokens are as fast as the host calls
+// tokens of 256 experts in BF16, sigmoid, 4 of 8 groups, top 8: 28.1 us
+// (17 MB in, 2 MB out: 3 us at the rate of a copy; softmax 31.4, with a bias
+// 33 and 36); wholly in binary64, with one token a wavefront, it was 94.  128 tokens are as fast as the host calls
 // (11 us).
 
 #include <hip/hip_runtime.h>
@@ -603,7 +603,7 @@ __device__ __forceinline__ float exp_diff(float x, float m) {
 // atomics.  Sums are binary32 (softmax's over all experts binary64); a BF16
 // gradient is rounded once, as it is stored.  Bounded by vector work and by its stores: 32768 tokens of 256
 // experts in binary32, sigmoid, top 8: 18 us for 34 MB written (6 us at the
-// rate of a fill).
+// rate of a fill); softmax without renormalisation, which reads them all, 26.
 template <typename Z, int EPL>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     const float* __restrict__ grad_w, const Z* __restrict__ logits, const int32_t* __restrict__ ids, int32_t T,
