@@ -44,6 +44,9 @@ from .api import (  # noqa: F401
     ep_dispatch,
     ep_dispatch_layout,
     ep_dispatch_layout_padded,
+    ep_expert_linear,
+    ep_expert_linear_backward,
+    ep_expert_linear_backward_weights,
     ep_expert_product,
     ep_layout_dispatch,
     ep_layout_dispatch_noalloc,
@@ -51,6 +54,9 @@ from .api import (  # noqa: F401
     ep_quantize_rows,
     ep_route,
     ep_route_backward,
+    expert_linear,
+    expert_linear_backward,
+    expert_linear_backward_weights,
     expert_product,
     layout,
     layout_padded,

@@ -55,6 +55,9 @@ EXPORTS = (
     "ep_quantize_rows",
     "ep_dequantize_rows",
     "ep_expert_product",
+    "ep_expert_linear",
+    "ep_expert_linear_backward",
+    "ep_expert_linear_backward_weights",
     "ep_cast_fp8_e4m3",
 )
 
@@ -116,6 +119,12 @@ def _load():
     lib.ep_dequantize_rows.restype = ctypes.c_int
     lib.ep_expert_product.argtypes = [p, p, i32, p, p, p, i64, i32, i32, i32, i32, i32, p, p]
     lib.ep_expert_product.restype = ctypes.c_int
+    lib.ep_expert_linear.argtypes = [p, p, p, p, p, i64, i32, i32, i32, i32, i32, p, p, p]
+    lib.ep_expert_linear.restype = ctypes.c_int
+    lib.ep_expert_linear_backward.argtypes = [p, p, p, p, i64, i32, i32, i32, i32, p, p]
+    lib.ep_expert_linear_backward.restype = ctypes.c_int
+    lib.ep_expert_linear_backward_weights.argtypes = [p, p, p, i64, i32, i32, i32, i32, i32, i32, p, p, p]
+    lib.ep_expert_linear_backward_weights.restype = ctypes.c_int
     lib.ep_cast_fp8_e4m3.argtypes = [p, p, i64, p]
     lib.ep_cast_fp8_e4m3.restype = ctypes.c_int
     return lib

@@ -509,6 +509,108 @@ def ep_expert_product(a, a_scale, format, w, w_scale, expert_rows, capacity, act
             R, E, cap, H, N, int(activation), y.data_ptr(), _stream(stream)))
 
 
+def _rows_shape(expert_rows, E, R, capacity):
+    """Checks of an expert layer's rows; the address of expert_rows, or None."""
+    if capacity < 0 or (capacity > 0 and R != E * capacity):
+        raise ValueError("capacity %d does not fit %d rows of %d experts" % (capacity, R, E))
+    if expert_rows is None:
+        if E != 1 or capacity != 0:
+            raise ValueError("without expert_rows there is one matrix and no capacity")
+        return None
+    _need(expert_rows, "expert_rows", _I32, (E,) if capacity else (E + 1,))
+    return expert_rows.data_ptr()
+
+
+def ep_expert_linear(a, w, expert_rows, capacity, activation, y, bias=None, residual=None, p=None, stream=None):
+    """y[r] = act(w[e(r)] @ a[r] + bias[e(r)]) + residual[r] in bf16.  a [rows,
+    H]; w [E, N, H]; bias [E, N] or None; expert_rows: as ep_expert_product's,
+    or None (E 1, capacity 0) where every row is the one matrix's; activation
+    EP_ACT_NONE (y [rows, N]) or EP_ACT_SWIGLU (y [rows, N/2]); residual of
+    y's shape or None, may be y itself; p [rows, N] or None (EP_ACT_SWIGLU)
+    receives the rows before the activation.  Rows of no expert are left
+    untouched."""
+    _need(w, "w", _BF16)
+    if w.dim() != 3:
+        raise ValueError("w must be [E, N, H]")
+    E, N, H = w.shape
+    if activation not in (EP_ACT_NONE, EP_ACT_SWIGLU):
+        raise ValueError("unknown activation %r" % (activation,))
+    gated = activation == EP_ACT_SWIGLU
+    if H % 8 or N % (16 if gated else 8):
+        raise ValueError("the layer needs hidden and out channels in multiples of 8, gate and up each")
+    _need(a, "a", _BF16)
+    if a.dim() != 2 or a.shape[1] != H:
+        raise ValueError("a must be [rows, %d]" % H)
+    R, cap = a.shape[0], int(capacity)
+    rows = _rows_shape(expert_rows, E, R, cap)
+    out = N // 2 if gated else N
+    _need(y, "y", _BF16, (R, out))
+    if bias is not None:
+        _need(bias, "bias", _BF16, (E, N))
+    if residual is not None:
+        _need(residual, "residual", _BF16, (R, out))
+    if p is not None:
+        if not gated:
+            raise ValueError("p belongs to a gated layer")
+        _need(p, "p", _BF16, (R, N))
+    with _device_of(a, w, expert_rows, bias, residual, p, y):
+        check("ep_expert_linear", LIB.ep_expert_linear(
+            a.data_ptr(), w.data_ptr(), bias.data_ptr() if bias is not None else None,
+            residual.data_ptr() if residual is not None else None, rows, R, E, cap, H, N, int(activation),
+            p.data_ptr() if p is not None else None, y.data_ptr(), _stream(stream)))
+
+
+def ep_expert_linear_backward(grad_y, w, expert_rows, capacity, grad_a, p=None, stream=None):
+    """Gradient of ep_expert_linear w.r.t. its rows: grad_y [rows, N] and w
+    [E, N, H] to grad_a [rows, H]; with p [rows, 2H], what the gated layer
+    before it kept, on to the gradient of p, grad_a [rows, 2H] (may be p
+    itself)."""
+    _need(w, "w", _BF16)
+    if w.dim() != 3:
+        raise ValueError("w must be [E, N, H]")
+    E, N, H = w.shape
+    if H % 8 or N % 8:
+        raise ValueError("the layer needs hidden and out channels in multiples of 8")
+    _need(grad_y, "grad_y", _BF16)
+    if grad_y.dim() != 2 or grad_y.shape[1] != N:
+        raise ValueError("grad_y must be [rows, %d]" % N)
+    R, cap = grad_y.shape[0], int(capacity)
+    rows = _rows_shape(expert_rows, E, R, cap)
+    if p is not None:
+        _need(p, "p", _BF16, (R, 2 * H))
+    _need(grad_a, "grad_a", _BF16, (R, 2 * H if p is not None else H))
+    with _device_of(grad_y, w, expert_rows, p, grad_a):
+        check("ep_expert_linear_backward", LIB.ep_expert_linear_backward(
+            grad_y.data_ptr(), w.data_ptr(), p.data_ptr() if p is not None else None, rows, R, E, cap, H, N,
+            grad_a.data_ptr(), _stream(stream)))
+
+
+def ep_expert_linear_backward_weights(grad_y, a, expert_rows, capacity, grad_w, grad_bias=None, accumulate=False,
+                                      stream=None):
+    """Gradients of ep_expert_linear w.r.t. its weights and biases: grad_y
+    [rows, N] and a [rows, H] (bf16) to grad_w [E, N, H] (float32 or bf16) and
+    grad_bias [E, N] (of the same type) or None; accumulate adds to what is
+    there.  Experts without rows get zeros."""
+    _need(grad_w, "grad_w", (torch.float32, torch.bfloat16))
+    if grad_w.dim() != 3:
+        raise ValueError("grad_w must be [E, N, H]")
+    E, N, H = grad_w.shape
+    if H % 8 or N % 8:
+        raise ValueError("the layer needs hidden and out channels in multiples of 8")
+    _need(grad_y, "grad_y", _BF16)
+    if grad_y.dim() != 2 or grad_y.shape[1] != N:
+        raise ValueError("grad_y must be [rows, %d]" % N)
+    R, cap = grad_y.shape[0], int(capacity)
+    _need(a, "a", _BF16, (R, H))
+    rows = _rows_shape(expert_rows, E, R, cap)
+    if grad_bias is not None:
+        _need(grad_bias, "grad_bias", (grad_w.dtype,), (E, N))
+    with _device_of(grad_y, a, expert_rows, grad_w, grad_bias):
+        check("ep_expert_linear_backward_weights", LIB.ep_expert_linear_backward_weights(
+            grad_y.data_ptr(), a.data_ptr(), rows, R, E, cap, H, N, _logits_dtype(grad_w), int(bool(accumulate)),
+            grad_w.data_ptr(), grad_bias.data_ptr() if grad_bias is not None else None, _stream(stream)))
+
+
 def ep_cast_fp8_e4m3(inp, out, stream=None):
     """The binary32 -> E4M3FN conversion dispatch uses (round to nearest
     even, saturating at +-448), elementwise: inp float32, out uint8 of the
@@ -721,3 +823,76 @@ def expert_product(a, a_scale, w, w_scale, handle, activation=EP_ACT_NONE, strea
     ep_expert_product(a2, s2, format, w, w_scale, handle.recv_expert_count if padded else handle.expert_offset,
                       handle.capacity if padded else 0, activation, y, stream)
     return y.view(handle.num_experts, handle.capacity, out) if padded else y
+
+
+def _flat(name, t):
+    if t.dim() < 2 or not t.is_contiguous():  # (a copy made here would be on the current stream, not on ``stream``)
+        raise ValueError("%s must be contiguous rows" % name)
+    return t.view(-1, t.shape[-1])
+
+
+def _expert_rows(handle):
+    """expert_rows and capacity of a handle (None: every row is one matrix's)."""
+    if handle is None:
+        return None, 0
+    if isinstance(handle, PaddedHandle):
+        return handle.recv_expert_count, handle.capacity
+    return handle.expert_offset, 0
+
+
+def _matrices(w):
+    return w.unsqueeze(0) if w.dim() == 2 else w  # (one matrix may come without its expert dimension)
+
+
+def _as_rows(t, handle):
+    return t.view(handle.num_experts, handle.capacity, -1) if isinstance(handle, PaddedHandle) else t
+
+
+def expert_linear(a, w, handle, bias=None, activation=EP_ACT_NONE, residual=None, save=False, stream=None):
+    """Every expert's bf16 layer on its rows -> bf16 [rows, N] (N/2 channels
+    with EP_ACT_SWIGLU), [E, capacity, ..] for a PaddedHandle.  a: as dispatch
+    (or low_latency_dispatch) returned it with ``handle`` in EP_RECV_BF16; w
+    [E, N, H], bias [E, N].  ``handle`` None: one matrix w ([N, H], or [1, N,
+    H]; bias [N] or [1, N]) for all rows, a shared expert's.  residual (of the
+    result's shape) is added behind the activation.  With save (EP_ACT_SWIGLU)
+    -> (y, p), p [rows, N] being what expert_linear_backward needs.  Rows of
+    no expert hold no defined values."""
+    rows, cap = _expert_rows(handle)
+    a2, w = _flat("a", a), _matrices(w)
+    if w.dim() != 3:
+        raise ValueError("w must be [E, N, H]")
+    N = w.shape[1]
+    y = torch.empty((a2.shape[0], N // 2 if activation == EP_ACT_SWIGLU else N), dtype=torch.bfloat16, device=a.device)
+    p = torch.empty((a2.shape[0], N), dtype=torch.bfloat16, device=a.device) if save else None
+    if bias is not None and bias.dim() == 1:
+        bias = bias.unsqueeze(0)
+    ep_expert_linear(a2, w, rows, cap, activation, y, bias, _flat("residual", residual) if residual is not None else None,
+                     p, stream)
+    return (_as_rows(y, handle), _as_rows(p, handle)) if save else _as_rows(y, handle)
+
+
+def expert_linear_backward(grad_y, w, handle, p=None, stream=None):
+    """Gradient of expert_linear w.r.t. its rows -> bf16 [rows, H]; with p, what
+    the gated layer that made those rows saved, the gradient of p -> [rows,
+    2H], which is that layer's grad_y."""
+    rows, cap = _expert_rows(handle)
+    g, w = _flat("grad_y", grad_y), _matrices(w)
+    if w.dim() != 3:
+        raise ValueError("w must be [E, N, H]")
+    H = w.shape[2]
+    grad_a = torch.empty((g.shape[0], 2 * H if p is not None else H), dtype=torch.bfloat16, device=grad_y.device)
+    ep_expert_linear_backward(g, w, rows, cap, grad_a, _flat("p", p) if p is not None else None, stream)
+    return _as_rows(grad_a, handle)
+
+
+def expert_linear_backward_weights(grad_y, a, handle, dtype=torch.bfloat16, bias=False, stream=None):
+    """Gradient of expert_linear w.r.t. its weights -> [E, N, H] of ``dtype``
+    (bfloat16 or float32; [1, N, H] for ``handle`` None); with bias -> (grad_w,
+    grad_bias [E, N])."""
+    rows, cap = _expert_rows(handle)
+    g, a2 = _flat("grad_y", grad_y), _flat("a", a)
+    E = handle.num_experts if handle is not None else 1
+    grad_w = torch.empty((E, g.shape[1], a2.shape[1]), dtype=dtype, device=grad_y.device)
+    grad_bias = torch.empty((E, g.shape[1]), dtype=dtype, device=grad_y.device) if bias else None
+    ep_expert_linear_backward_weights(g, a2, rows, cap, grad_w, grad_bias, False, stream)
+    return (grad_w, grad_bias) if bias else grad_w

@@ -514,6 +514,21 @@ ep_status check_rows(const void* x, int64_t rows, int32_t H, int32_t format, con
   return EP_OK;
 }
 
+// Sizes of an expert's bf16 layer; widest: channels of the widest rows.
+ep_status check_linear(const int32_t* expert_rows, int64_t rows, int32_t E, int32_t capacity, int32_t H, int32_t N,
+                       int64_t widest) {
+  if (rows < 0 || E < 1 || capacity < 0 || H <= 0 || N <= 0 || H % 8 != 0 || N % 8 != 0) return EP_ERR_INVALID_ARG;
+  if (E > EP_MAX_EXPERTS || H > 65536 || N > 65536) return EP_ERR_UNSUPPORTED;
+  if (rows >= (int64_t(1) << 31) || rows * widest >= kMaxElems) return EP_ERR_UNSUPPORTED;
+  if (capacity > 0 && rows != static_cast<int64_t>(E) * capacity) return EP_ERR_INVALID_ARG;
+  if (expert_rows == nullptr && (E != 1 || capacity != 0)) return EP_ERR_INVALID_ARG;
+  if (!aligned(expert_rows, 4)) return EP_ERR_INVALID_ARG;
+  return EP_OK;
+}
+
+const uint16_t* bf16(const void* p) { return static_cast<const uint16_t*>(p); }
+uint16_t* bf16(void* p) { return static_cast<uint16_t*>(p); }
+
 }  // namespace
 
 EP_API ep_status ep_route(const void* logits, int32_t logits_dtype, const float* bias, int64_t num_tokens,
@@ -583,6 +598,58 @@ EP_API ep_status ep_expert_product(const void* a, const void* a_scale, int32_t a
                                             static_cast<int32_t>(num_rows), num_experts, capacity, hidden,
                                             out_channels, gated, static_cast<uint16_t*>(y),
                                             static_cast<hipStream_t>(stream)));
+}
+
+EP_API ep_status ep_expert_linear(const void* a, const void* w, const void* bias, const void* residual,
+                                  const int32_t* expert_rows, int64_t num_rows, int32_t num_experts, int32_t capacity,
+                                  int32_t hidden, int32_t out_channels, int32_t activation, void* p, void* y,
+                                  void* stream) {
+  if (activation != EP_ACT_NONE && activation != EP_ACT_SWIGLU) return EP_ERR_INVALID_ARG;
+  const bool gated = activation == EP_ACT_SWIGLU;
+  const ep_status st = check_linear(expert_rows, num_rows, num_experts, capacity, hidden, out_channels,
+                                    hidden > out_channels ? hidden : out_channels);
+  if (st != EP_OK) return st;
+  if ((gated && out_channels % 16 != 0) || (!gated && p != nullptr)) return EP_ERR_INVALID_ARG;
+  if (num_rows == 0) return EP_OK;
+  if (!a || !w || !y) return EP_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(p, 16) ||
+      !aligned(y, 16))
+    return EP_ERR_INVALID_ARG;
+  return from_hip(ep::launch_expert_linear(bf16(a), bf16(w), bf16(bias), bf16(residual), expert_rows,
+                                           static_cast<int32_t>(num_rows), num_experts, capacity, hidden, out_channels,
+                                           gated, bf16(p), bf16(y), static_cast<hipStream_t>(stream)));
+}
+
+EP_API ep_status ep_expert_linear_backward(const void* grad_y, const void* w, const void* p,
+                                           const int32_t* expert_rows, int64_t num_rows, int32_t num_experts,
+                                           int32_t capacity, int32_t hidden, int32_t out_channels, void* grad_a,
+                                           void* stream) {
+  const int64_t wide = static_cast<int64_t>(hidden) * (p != nullptr ? 2 : 1);
+  const ep_status st = check_linear(expert_rows, num_rows, num_experts, capacity, hidden, out_channels,
+                                    wide > out_channels ? wide : out_channels);
+  if (st != EP_OK || num_rows == 0) return st;
+  if (!grad_y || !w || !grad_a) return EP_ERR_INVALID_ARG;
+  if (!aligned(grad_y, 16) || !aligned(w, 16) || !aligned(p, 16) || !aligned(grad_a, 16)) return EP_ERR_INVALID_ARG;
+  return from_hip(ep::launch_expert_linear_backward(bf16(grad_y), bf16(w), bf16(p), expert_rows,
+                                                    static_cast<int32_t>(num_rows), num_experts, capacity, hidden,
+                                                    out_channels, bf16(grad_a), static_cast<hipStream_t>(stream)));
+}
+
+EP_API ep_status ep_expert_linear_backward_weights(const void* grad_y, const void* a, const int32_t* expert_rows,
+                                                   int64_t num_rows, int32_t num_experts, int32_t capacity,
+                                                   int32_t hidden, int32_t out_channels, int32_t grad_dtype,
+                                                   int32_t accumulate, void* grad_w, void* grad_bias, void* stream) {
+  if (grad_dtype != EP_DTYPE_F32 && grad_dtype != EP_DTYPE_BF16) return EP_ERR_INVALID_ARG;
+  const ep_status st = check_linear(expert_rows, num_rows, num_experts, capacity, hidden, out_channels,
+                                    hidden > out_channels ? hidden : out_channels);
+  if (st != EP_OK) return st;
+  if (!grad_w || (num_rows > 0 && (!grad_y || !a))) return EP_ERR_INVALID_ARG;
+  if (!aligned(grad_y, 16) || !aligned(a, 16) || !aligned(grad_w, 16) || !aligned(grad_bias, 16))
+    return EP_ERR_INVALID_ARG;
+  if (num_rows == 0 && accumulate != 0) return EP_OK;
+  return from_hip(ep::launch_expert_linear_backward_weights(
+      bf16(grad_y), bf16(a), expert_rows, static_cast<int32_t>(num_rows), num_experts, capacity, hidden, out_channels,
+      grad_dtype == EP_DTYPE_BF16, accumulate != 0, grad_w, grad_bias, static_cast<hipStream_t>(stream)));
 }
 
 EP_API ep_status ep_cast_fp8_e4m3(const float* in, uint8_t* out, int64_t n, void* stream) {

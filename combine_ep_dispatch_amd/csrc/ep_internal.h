@@ -51,6 +51,21 @@ hipError_t launch_expert_product(const void* a, const void* a_scale, bool fp8, c
                                  const int32_t* expert_rows, int32_t num_rows, int32_t num_experts, int32_t capacity,
                                  int32_t hidden, int32_t out_channels, bool gated, uint16_t* y, hipStream_t stream);
 
+// The experts' bf16 layers and their gradients (expert_rows null: every row
+// is expert 0's; bias, residual, p and grad_bias may be null).
+hipError_t launch_expert_linear(const uint16_t* a, const uint16_t* w, const uint16_t* bias, const uint16_t* residual,
+                                const int32_t* expert_rows, int32_t num_rows, int32_t num_experts, int32_t capacity,
+                                int32_t hidden, int32_t out_channels, bool gated, uint16_t* p, uint16_t* y,
+                                hipStream_t stream);
+hipError_t launch_expert_linear_backward(const uint16_t* grad_y, const uint16_t* w, const uint16_t* p,
+                                         const int32_t* expert_rows, int32_t num_rows, int32_t num_experts,
+                                         int32_t capacity, int32_t hidden, int32_t out_channels, uint16_t* grad_a,
+                                         hipStream_t stream);
+hipError_t launch_expert_linear_backward_weights(const uint16_t* grad_y, const uint16_t* a, const int32_t* expert_rows,
+                                                 int32_t num_rows, int32_t num_experts, int32_t capacity,
+                                                 int32_t hidden, int32_t out_channels, bool bf16, bool add,
+                                                 void* grad_w, void* grad_bias, hipStream_t stream);
+
 // The burst fan-out of BF16 token rows (from 16 MB of tokens): out[slot[t,k]]
 // = x[t] (weighted: BF16_RNE(RN32(w[t,k] * x[t])) per channel); returns false,
 // launching nothing, below its size or where the device's CU count is unknown.

@@ -19,29 +19,16 @@
 
 #include "ep_device.h"
 #include "ep_internal.h"
-#include "expert_rows.h"
+#include "expert_device.h"
 #include "mx_device.h"
 
 namespace ep {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFp4 = 4, kFp8 = 0;  // operand formats of the scaled MFMA
 constexpr int kThreads = 256;
-constexpr int kMaxExperts = 1024;
-
-// Rows of expert e: [first, first + count), clamped to the buffer.
-__device__ __forceinline__ void rows_of(const int32_t* __restrict__ expert_rows, int e, int capacity, int num_rows,
-                                        int& first, int& count) {
-  if (capacity > 0) {
-    first = e * capacity;
-    count = min(max(expert_rows[e], 0), capacity);
-  } else {
-    span_rows(expert_rows[e], expert_rows[e + 1], num_rows, first, count);
-  }
-}
 
 // FP8 codes below 2 in magnitude, and those of 2 and more; zeros elsewhere.
 // The matrix unit adds the products of eight neighbouring channels in one step
@@ -60,31 +47,6 @@ __device__ __forceinline__ void split_codes(i32x8 x, i32x8& low, i32x8& high) {
     high[i] = static_cast<int>(v & m);
     low[i] = static_cast<int>(v & ~m);
   }
-}
-
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
-
-// start[0 .. E] to the sums before each, by the workgroup's first wavefront;
-// every thread must call it.
-__device__ __forceinline__ void tiles_before(RowTiles* start, int E) {
-  if (threadIdx.x < kWave) {
-    const int per = E / kWave + 1, beg = threadIdx.x * per, end = min(beg + per, E + 1);
-    RowTiles mine = 0;
-    for (int e = beg; e < end; ++e) mine += start[e];
-    RowTiles run = mine;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const RowTiles o = __shfl_up(run, d);
-      if (static_cast<int>(threadIdx.x) >= d) run += o;
-    }
-    run -= mine;
-    for (int e = beg; e < end; ++e) {
-      const RowTiles n = start[e];
-      start[e] = run;
-      run += n;
-    }
-  }
-  __syncthreads();
 }
 
 template <bool FP8, bool GATED>
@@ -179,58 +141,12 @@ __global__ __launch_bounds__(kThreads) void product_kernel(const uint8_t* __rest
 // both in the largest tile, which has no registers left (4642 against 4951
 // us), and where three stages of 256 weight rows leave no LDS.
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef __amdgpu_buffer_rsrc_t Rsrc;
-typedef __attribute__((address_space(3))) void LdsVoid;
-
-__device__ __forceinline__ Rsrc make_rsrc(const void* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes), 0x00027000);
-}
-
-// 64 lanes x 16 bytes: lane l's piece lands at dst + 16 l.
-__device__ __forceinline__ void copy16(Rsrc src, uint8_t* dst, uint32_t lane_off, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (LdsVoid*)dst, 16, lane_off, off, 0, 0);
-}
-// The same, non-temporal.
-__device__ __forceinline__ void copy16_once(Rsrc src, uint8_t* dst, uint32_t lane_off, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (LdsVoid*)dst, 16, lane_off, off, 0, 2);
-}
-
-// Until at most N of this wave's copies are under way (they finish in order)
-// and its LDS reads are done; then the workgroup's barrier.
-template <int N>
-__device__ __forceinline__ void wait_and_sync() {
-  static_assert(N < 16, "vmcnt");
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(N | 7 << 4);  // vmcnt(N) lgkmcnt(0)
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 __device__ __forceinline__ uint32_t swizzle8(uint32_t row) { return (row & 7) ^ ((row >> 3) & 1); }
 __device__ __forceinline__ uint32_t swizzle16(uint32_t row) { return row & 15; }
 
 __device__ __forceinline__ i32x8 widen(u32x4 lo) {
   return i32x8{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]), static_cast<int>(lo[3]),
                0, 0, 0, 0};
-}
-
-// The workgroup's barrier once this wave's LDS reads are done.
-__device__ __forceinline__ void wait_reads() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(15 | 7 << 4 | 3 << 14);  // lgkmcnt(0)
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
-// f(0) && f(1) && ...
-template <int I, int N, typename F>
-__device__ __forceinline__ bool static_while(F&& f) {
-  if constexpr (I < N) {
-    if (!f(std::integral_constant<int, I>{})) return false;
-    return static_while<I + 1, N>(f);
-  }
-  return true;
 }
 
 // An offset past the end of every operand (at most 2^31 bytes of one expert's

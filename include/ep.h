@@ -69,7 +69,7 @@ typedef enum { EP_DTYPE_F32 = 0, EP_DTYPE_BF16 = 1 } ep_dtype;
 /* How ep_route turns logits into scores. */
 typedef enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 } ep_score;
 
-/* What ep_expert_product does with its sums. */
+/* What ep_expert_product and ep_expert_linear do with their sums. */
 typedef enum { EP_ACT_NONE = 0, EP_ACT_SWIGLU = 1 } ep_activation;
 
 #define EP_MAX_EXPERTS 1024
@@ -494,6 +494,74 @@ ep_status ep_expert_product(const void* a, const void* a_scale, int32_t a_format
                             const void* w_scale, const int32_t* expert_rows, int64_t num_rows, int32_t num_experts,
                             int32_t capacity, int32_t hidden, int32_t out_channels, int32_t activation, void* y,
                             void* stream);
+
+/*
+ * ep_expert_linear - every expert's bf16 layer on the rows the dispatch gave
+ * it (EP_RECV_BF16), or one layer on all rows, as a shared expert's:
+ *   p[r, n] = sum_h w[e(r), n, h] * a[r, h] + bias[e(r), n]
+ *   y[r, n] = BF16_RNE(p[r, n] + residual[r, n])                              EP_ACT_NONE
+ *   y[r, i] = BF16_RNE(silu(p[r, i]) * p[r, N/2 + i] + residual[r, i])        EP_ACT_SWIGLU
+ * silu(u) = u / (1 + exp(-u)).  Products are exact; sums, bias, activation
+ * and residual are binary32, rounded once at the end (y does not see p's
+ * rounding).
+ *
+ * a            bf16 [num_rows, H]
+ * w            bf16 [E, N, H]
+ * bias         bf16 [E, N] or NULL
+ * residual     bf16 of y's shape or NULL; may be y itself
+ * expert_rows  as ep_expert_product's; NULL (E == 1, capacity == 0): every
+ *              row is expert 0's
+ * p            bf16 [num_rows, N] out or NULL: p rounded to BF16, what
+ *              ep_expert_linear_backward needs of a gated layer
+ *              (EP_ACT_SWIGLU only)
+ * y            bf16 [num_rows, N] (N/2 with EP_ACT_SWIGLU) out
+ * Rows of no expert are left untouched.  No output overlaps an input (but y
+ * its residual) or the other output.  All bf16 arrays 16-byte aligned.
+ * Requirements: 1 <= E <= EP_MAX_EXPERTS, H % 8 == 0, N % 8 == 0 (N % 16 ==
+ * 0 with EP_ACT_SWIGLU), H and N <= 65536, num_rows < 2^31, num_rows *
+ * max(H, N) < 2^34.
+ */
+ep_status ep_expert_linear(const void* a, const void* w, const void* bias, const void* residual,
+                           const int32_t* expert_rows, int64_t num_rows, int32_t num_experts, int32_t capacity,
+                           int32_t hidden, int32_t out_channels, int32_t activation, void* p, void* y, void* stream);
+
+/*
+ * ep_expert_linear_backward - gradient of ep_expert_linear w.r.t. its rows:
+ *   d[r, h] = sum_n w[e(r), n, h] * grad_y[r, n]
+ *   grad_a[r, h] = BF16_RNE(d[r, h])                                           p NULL
+ * or, where the rows a were themselves the gated activation of a layer that
+ * kept p [num_rows, 2H] = (g | u), on through it to the gradient of p:
+ *   grad_a[r, h]     = BF16_RNE(d[r, h] * u[r, h] * s (1 + g (1 - s)))
+ *   grad_a[r, H + h] = BF16_RNE(d[r, h] * g s),     s = 1 / (1 + exp(-g[r, h]))
+ * in binary32.  (grad_y here is the gradient of p for a gated layer, of y
+ * for one without activation; a residual's gradient is grad_y itself.)
+ *
+ * grad_y bf16 [num_rows, N]; w bf16 [E, N, H]; p bf16 [num_rows, 2H] or
+ * NULL; grad_a bf16 [num_rows, H], or [num_rows, 2H] with p, out, which may
+ * be p itself; else as for ep_expert_linear, with num_rows * 2H < 2^34 where
+ * p is given.
+ */
+ep_status ep_expert_linear_backward(const void* grad_y, const void* w, const void* p, const int32_t* expert_rows,
+                                    int64_t num_rows, int32_t num_experts, int32_t capacity, int32_t hidden,
+                                    int32_t out_channels, void* grad_a, void* stream);
+
+/*
+ * ep_expert_linear_backward_weights - gradients of ep_expert_linear w.r.t.
+ * its weights and biases, over each expert's rows in a fixed order:
+ *   grad_w[e, n, h] = sum_{r of e} grad_y[r, n] * a[r, h]
+ *   grad_bias[e, n] = sum_{r of e} grad_y[r, n]
+ * in binary32; with accumulate != 0 the sum is added to what is there, and
+ * rounded once.  An expert without rows gets zeros (keeps what is there).
+ *
+ * grad_y bf16 [num_rows, N]; a bf16 [num_rows, H]; grad_w [E, N, H] out, of
+ * type grad_dtype (EP_DTYPE_F32 or EP_DTYPE_BF16); grad_bias [E, N] out, of
+ * the same type, or NULL; all 16-byte aligned; else as for ep_expert_linear
+ * (num_rows == 0 writes zeros).
+ */
+ep_status ep_expert_linear_backward_weights(const void* grad_y, const void* a, const int32_t* expert_rows,
+                                            int64_t num_rows, int32_t num_experts, int32_t capacity, int32_t hidden,
+                                            int32_t out_channels, int32_t grad_dtype, int32_t accumulate,
+                                            void* grad_w, void* grad_bias, void* stream);
 
 /*
  * ep_cast_fp8_e4m3 - the binary32 -> E4M3FN conversion ep_dispatch uses,

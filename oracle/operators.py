@@ -209,3 +209,78 @@ def expert_product(a, w, spans, gated):
         else:
             y[first:first + count], mag[first:first + count] = p, m
     return y, mag
+
+
+# ---- the experts' bf16 layers ------------------------------------------------
+
+def sigmoid(g):
+    e = np.exp(-np.abs(g))
+    return np.where(g < 0, e, 1.0) / (1.0 + e)
+
+
+def expert_linear(a, w, bias, residual, spans, gated):
+    """a float64 [R, H], w [E, N, H], bias [E, N] or None, residual or None,
+    spans [(first, count)] -> {"y": (value, bound), "p": (value, bound)}: the
+    rows before their rounding to BF16 (NaN in rows of no expert), and how far
+    binary32 sums may be off: every one of the H + 1 additions of a sum by at
+    most 2^-23 of the terms' magnitudes, the activation by (|g| + 8) 2^-23 of
+    its value (an exponential of g, whose argument is rounded, a sum, a
+    reciprocal and two products)."""
+    R, H, N = a.shape[0], w.shape[2], w.shape[1]
+    O = N // 2 if gated else N
+    out = {k: (np.full((R, n), np.nan), np.full((R, n), np.nan)) for k, n in (("y", O), ("p", N))}
+    for e, (first, count) in enumerate(spans):
+        at = slice(first, first + count)
+        p, m = a[at] @ w[e].T, np.abs(a[at]) @ np.abs(w[e]).T
+        if bias is not None:
+            p, m = p + bias[e], m + np.abs(bias[e])
+        err = (H + 1) * 2.0 ** -23 * m
+        out["p"][0][at], out["p"][1][at] = p, err
+        if gated:
+            g, u, eg, eu = p[:, :O], p[:, O:], err[:, :O], err[:, O:]
+            s = g * sigmoid(g)
+            p = s * u
+            err = 1.1 * eg * (np.abs(u) + eu) + np.abs(s) * eu + (np.abs(g) + 8) * 2.0 ** -23 * np.abs(p)  # |silu'| <= 1.1
+        if residual is not None:
+            p = p + residual[at]
+            err = err + 2.0 ** -23 * (np.abs(p) + np.abs(residual[at]))
+        out["y"][0][at], out["y"][1][at] = p, err
+    return out
+
+
+def expert_linear_backward(grad_y, w, p, spans):
+    """-> (gradient of the rows, or of p where it is given, bound): as
+    expert_linear; the slopes of the activation are off by (|g| + 8) 2^-23 of
+    their terms."""
+    R, N, H = grad_y.shape[0], w.shape[1], w.shape[2]
+    val, bound = np.full((R, H if p is None else 2 * H), np.nan), np.full((R, H if p is None else 2 * H), np.nan)
+    for e, (first, count) in enumerate(spans):
+        at = slice(first, first + count)
+        d, err = grad_y[at] @ w[e], N * 2.0 ** -23 * (np.abs(grad_y[at]) @ np.abs(w[e]))
+        if p is None:
+            val[at], bound[at] = d, err
+            continue
+        g, u = p[at, :H], p[at, H:]
+        s, n = sigmoid(g), sigmoid(-g)
+        rel = (np.abs(g) + 8) * 2.0 ** -23
+        slope, terms = s * (1 + g * n), s * (1 + np.abs(g) * n)
+        val[at, :H], val[at, H:] = d * u * slope, d * g * s
+        bound[at, :H] = np.abs(u) * (err * np.abs(slope) + rel * (np.abs(d) + err) * terms)
+        bound[at, H:] = np.abs(g * s) * (err + rel * (np.abs(d) + err))
+    return val, bound
+
+
+def expert_linear_backward_weights(grad_y, a, spans, old_w=None, old_b=None):
+    """-> {"w": (value, bound), "b": (value, bound)}: sums over each expert's
+    rows, added to the old gradients where they are given."""
+    N, H = grad_y.shape[1], a.shape[1]
+    w, b = np.zeros((2, len(spans), N, H)), np.zeros((2, len(spans), N))
+    for e, (first, count) in enumerate(spans):
+        at = slice(first, first + count)
+        w[0, e], w[1, e] = grad_y[at].T @ a[at], (count + 1) * 2.0 ** -23 * (np.abs(grad_y[at]).T @ np.abs(a[at]))
+        b[0, e], b[1, e] = grad_y[at].sum(axis=0), (count + 1) * 2.0 ** -23 * np.abs(grad_y[at]).sum(axis=0)
+    for x, old in ((w, old_w), (b, old_b)):
+        if old is not None:
+            x[0] += old
+            x[1] += 2.0 ** -23 * (np.abs(x[0]) + np.abs(old))
+    return {"w": (w[0], w[1]), "b": (b[0], b[1])}
