@@ -22,7 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libep.so")
 SOURCES = ["ep_api.hip", "layout.hip", "layout_dispatch.hip", "dispatch.hip", "fused.hip", "combine.hip",
            "combine_backward.hip", "rows.hip", "route.hip", "expert_product.hip",
-           "expert_linear.hip"]
+           "expert_linear.hip", "expert_linear_backward.hip", "expert_linear_weights.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

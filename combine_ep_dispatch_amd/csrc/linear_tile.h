@@ -1,0 +1,642 @@
+// The tiled product of the experts' bf16 layers (internal header): forward,
+// the rows' gradient and the weights' gradient are one kernel, whose operands
+// lie differently in memory.
+//
+// A tile of the result is BM rows x BN channels.  Its channels' operand (X) is
+// the MFMA's A operand, its rows' (R) the B operand; both pass through LDS in
+// stages of 64 summed elements, copied straight from global memory some stages
+// ahead.
+//
+//            result            X                          R            summed over
+//   kForward y [row][n]        w [n][h], along h          a [row][h]   h
+//   kRows    grad_a [row][h]   w [n][h], across n         g [row][n]   n
+//   kWeights grad_w [n][h]     a [row][h], across rows    g [row][n]   an expert's rows
+//
+// An operand whose rows run along the summed index lies in LDS as rows of 128
+// bytes and is read 16 bytes (eight elements) a lane.  One that runs across
+// it lies as 64 rows of BN (BM) elements and is read through gfx950's
+// transposing LDS load: sixteen lanes read four rows of sixteen elements, and
+// each gets the four of its column.  Both kinds hold their 16-byte pieces
+// permuted, so that lanes served together meet different banks.
+#pragma once
+
+#include "ep_internal.h"
+#include "expert_device.h"
+
+namespace ep {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
+enum Kind { kForward, kRows, kWeights };
+
+struct LinearArgs {
+  const __bf16* x;         // w (kForward, kRows) or a
+  const __bf16* r;         // a, or the output's gradient
+  const __bf16* bias;      // or null (kForward)
+  const __bf16* residual;  // or null (kForward); may be y
+  const int32_t* expert_rows;
+  int32_t num_rows, E, capacity;
+  int32_t C;  // summed channels (not kWeights)
+  int32_t O;  // channels of the result (kForward gated: of y; kRows gated: of d)
+  int32_t M;  // rows of the result of one expert (kWeights: out channels)
+  bool add;   // kWeights: add to what is there
+  __bf16* p;  // kForward gated: out or null; kRows gated: in, may be y
+  void* y;
+};
+
+// Rows of expert e; without expert_rows every row is expert 0's.
+__device__ __forceinline__ void span_of(const int32_t* __restrict__ expert_rows, int e, int capacity, int num_rows,
+                                        int& first, int& count) {
+  if (expert_rows == nullptr) {
+    first = 0;
+    count = num_rows;
+  } else {
+    rows_of(expert_rows, e, capacity, num_rows, first, count);
+  }
+}
+
+// The gate's sigmoid s = 1 / (1 + exp(-g)) as two factors s1 s2, and n = 1 - s,
+// each without cancellation.  (Two, each with half the exponent, so that s
+// keeps its accuracy below 2^-126, where a large g or d makes it count.)
+struct Gate {
+  float s1, s2, n;
+};
+__device__ __forceinline__ Gate gate(float g) {
+  const float h = __expf(-0.5f * __builtin_fabsf(g)), e = h * h;
+  const float r = __builtin_amdgcn_rcpf(1.0f + e);
+  const bool low = g < 0.0f;
+  return Gate{low ? h : 1.0f, low ? h * r : r, low ? r : e * r};
+}
+__device__ __forceinline__ float silu_times(float g, float u) {
+  const Gate k = gate(g);
+  return (g * k.s1) * (u * k.s2);
+}
+
+// Until at most N of this wave's copies are under way (they finish in order)
+// and its LDS reads are done; then the workgroup's barrier.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  static_assert(N < 64, "vmcnt");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | (N >> 4) << 14);  // vmcnt(N) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// 16-byte pieces of 128-byte rows: eight rows, and the eight beyond, differ.
+__device__ __forceinline__ uint32_t along_swizzle(uint32_t row) { return (row & 7) ^ ((row >> 3) & 1); }
+// Pairs of pieces of the rows that a transposing load reads together.
+__device__ __forceinline__ uint32_t across_swizzle(uint32_t k) { return ((k & 3) | (k & 1) << 2) * 2; }
+
+// A value that is the same in every lane, kept where the compiler knows it (a
+// branch on anything else is taken for one that lanes take apart, and then the
+// copies of both its sides are waited for).
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+template <typename T>
+__device__ __forceinline__ T* uniform(T* p) {
+  return reinterpret_cast<T*>(uniform(reinterpret_cast<int64_t>(p)));
+}
+
+template <bool ONCE>
+__device__ __forceinline__ void copy_piece(Rsrc src, uint8_t* dst, uint32_t lane_off, uint32_t off) {
+  if constexpr (ONCE) copy16_once(src, dst, lane_off, off);
+  else copy16(src, dst, lane_off, off);
+}
+
+// A lane offset past the end of every operand's buffer resource (at most 2^25
+// bytes): loads from there give 0.
+constexpr uint32_t kNone = 0x80000000u;
+
+// WM x WN: the tile's waves; XS, RS: stages of X and of R kept; PER: workgroups
+// of a CU; ONCE: X is read non-temporally.
+template <Kind KIND, bool GATED, typename T, int BM, int BN, int WM, int WN, int XS, int RS, int PER, bool ONCE>
+__global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear_tiled(const LinearArgs g) {
+  constexpr int NW = WM * WN;
+  constexpr bool kPair = KIND == kForward && GATED;  // X holds gate and up rows of the same BO channels
+  constexpr bool kXAlong = KIND == kForward, kRAlong = KIND != kWeights;
+  constexpr int BO = kPair ? BN / 2 : BN;
+  constexpr int TN = BN / WN, FN = TN / 32, FM = BM / WM / 32;  // fragments of 32
+  constexpr int LX = BN / 8 / NW, LR = BM / 8 / NW;             // copies per wave and stage, 1 KB each
+  static_assert(LX * 8 * NW == BN && LR * 8 * NW == BM && FM * 32 * WM == BM && FN * 32 * WN == BN && NW % 2 == 0, "tile");
+  static_assert(!kPair || (FN % 2 == 0 && LX % 2 == 0), "a wave holds, and copies, both halves of its channels");
+  static_assert((kXAlong || BN >= 128) && (kRAlong || BM >= 128), "across_swizzle permutes 16 pieces");
+  static_assert(BN * 128 >= NW * 4096, "y's fragments");
+  static_assert(XS == RS || XS == RS + 1, "the order of the copies");
+  constexpr int kRing = XS == RS ? XS : XS * RS;  // stages after which the buffers repeat
+  static_assert(XS <= 6 && RS <= 6, "buffers");
+#define EP_BUFFER(name, i, n, rows) __shared__ __align__(16) uint8_t name##i[(n) > i ? (rows) * 128 : 16]
+  EP_BUFFER(x, 0, XS, BN);  // (arrays of their own: the compiler tells copies into one from reads of another)
+  EP_BUFFER(x, 1, XS, BN);
+  EP_BUFFER(x, 2, XS, BN);
+  EP_BUFFER(x, 3, XS, BN);
+  EP_BUFFER(x, 4, XS, BN);
+  EP_BUFFER(x, 5, XS, BN);
+  EP_BUFFER(r, 0, RS, BM);
+  EP_BUFFER(r, 1, RS, BM);
+  EP_BUFFER(r, 2, RS, BM);
+  EP_BUFFER(r, 3, RS, BM);
+  EP_BUFFER(r, 4, RS, BM);
+  EP_BUFFER(r, 5, RS, BM);
+#undef EP_BUFFER
+  const auto x_buf = [&](auto qc) -> uint8_t* {
+    constexpr int q = decltype(qc)::value % XS;
+    if constexpr (q == 0) return x0;
+    else if constexpr (q == 1) return x1;
+    else if constexpr (q == 2) return x2;
+    else if constexpr (q == 3) return x3;
+    else if constexpr (q == 4) return x4;
+    else return x5;
+  };
+  const auto r_buf = [&](auto qc) -> uint8_t* {
+    constexpr int q = decltype(qc)::value % RS;
+    if constexpr (q == 0) return r0;
+    else if constexpr (q == 1) return r1;
+    else if constexpr (q == 2) return r2;
+    else if constexpr (q == 3) return r3;
+    else if constexpr (q == 4) return r4;
+    else return r5;
+  };
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int half = lane >> 5, col = lane & 31;
+  const int wm = wave % WM, wn = wave / WM;
+  const int O = g.O;
+  const uint32_t nt = (O + BO - 1) / BO;
+  const int E = g.E;
+
+  // ---- tiles ----
+  // kForward, kRows: the row tiles of each expert times nt; they go in eight
+  // runs, one per XCD (workgroups go to the XCDs in turn), so that neighbouring
+  // tiles, which share weights or rows, meet in one L2.  Each wavefront finds its
+  // first one from sums over E / 64 experts a lane, and walks on from there.
+  // kWeights: every expert has the same tiles, but sums of its own length; they
+  // are dealt out in turns of one a workgroup, each XCD's next to one another.
+  const auto row_tiles = [&](int e) -> uint32_t {
+    int first, count;
+    span_of(g.expert_rows, e, g.capacity, g.num_rows, first, count);
+    return (static_cast<uint32_t>(count) + BM - 1) / BM;
+  };
+  uint32_t tile, end, step, te = 0;
+  int64_t before = 0;  // row tiles before expert `walk`
+  int walk = 0;
+  if constexpr (KIND == kWeights) {
+    te = (g.M + BM - 1) / BM;
+    const uint64_t all = static_cast<uint64_t>(te) * nt * E;
+    end = static_cast<uint32_t>(min(all, static_cast<uint64_t>(0x40000000)));
+    step = gridDim.x;
+    tile = (blockIdx.x & 7) * (gridDim.x / 8) + blockIdx.x / 8;
+    if (tile >= end) return;
+  } else {
+    int64_t mine = 0;
+    const int per = (E + kWave - 1) / kWave;  // experts of a lane
+    for (int i = 0; i < per; i += 4) {
+      uint32_t n[4];  // (loaded for any lane, so that the four loads overlap)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) n[x] = row_tiles(min(lane * per + i + x, E - 1));
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mine += i + x < per && lane * per + i + x < E ? n[x] : 0;
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int64_t o = __shfl_up(upto, d);
+      if (lane >= d) upto += o;
+    }
+    // (2^30 tiles at most: rows that lie apart make far fewer)
+    const uint64_t all = static_cast<uint64_t>(__shfl(upto, kWave - 1)) * nt;
+    const uint32_t tiles = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(min(all, static_cast<uint64_t>(0x40000000))));
+    const uint32_t run = (tiles + 7) / 8;
+    step = gridDim.x / 8;
+    end = min((blockIdx.x & 7) * run + run, tiles);
+    tile = (blockIdx.x & 7) * run + blockIdx.x / 8;
+    if (tile >= end) return;
+    // the first lane that ends beyond this tile's row tile holds its expert
+    const int at = __builtin_ctzll(wave_ballot(upto > static_cast<int64_t>(tile / nt)));
+    before = uniform(__shfl(upto - mine, at));
+    walk = __builtin_amdgcn_readfirstlane(at * per);
+    te = __builtin_amdgcn_readfirstlane(row_tiles(walk));
+  }
+
+  // ---- the tile whose stages are being copied ----
+  struct Place {
+    int e, first, count, m0, n0;  // expert, its rows, the tile's first row and channel
+  } at;
+  // An expert's tiles go in bands of eight row tiles, channel by channel, so that
+  // the 32 workgroups of an XCD read 8 + 4 operands' tiles at a time.
+  const auto place = [&](uint32_t local) {
+    const uint32_t band = local / (8 * nt), rest = local - band * 8 * nt, width = min(te - band * 8, 8u);
+    at.m0 = static_cast<int>(band * 8 + rest % width) * BM;
+    at.n0 = static_cast<int>(rest / width) * BO;
+  };
+  const auto open_tile = [&]() {
+    if constexpr (KIND == kWeights) {
+      const uint32_t each = te * nt;
+      at.e = tile / each;
+      const uint32_t local = tile - at.e * each;
+      place(local);
+    } else {
+      const uint32_t q = tile / nt;
+      while (q >= static_cast<uint64_t>(before + te)) {  // ends at the expert of tile q
+        before += te;
+        te = __builtin_amdgcn_readfirstlane(row_tiles(++walk));
+      }
+      at.e = walk;
+      const uint32_t local = tile - static_cast<uint32_t>(before) * nt;
+      place(local);
+    }
+    span_of(g.expert_rows, at.e, g.capacity, g.num_rows, at.first, at.count);
+    at.first = __builtin_amdgcn_readfirstlane(at.first);
+    at.count = __builtin_amdgcn_readfirstlane(at.count);
+  };
+  const auto stages_of = [&](const Place& t) { return ((KIND == kWeights ? t.count : g.C) + 63) / 64; };
+  const auto rows_in = [&](const Place& t) { return min((KIND == kWeights ? g.M : t.count) - t.m0, BM); };
+
+  // An operand's copies.  Along: piece (lane & 7) of row lane / 8 of eight, and
+  // the last stage's pieces past the end are read past the end of the buffer
+  // resource (kNone), which gives zeros.  Across: a stage is a buffer resource of
+  // its own, which ends with its last row.
+  const uint32_t along_piece = (lane & 7) ^ along_swizzle((wave & 1) * 8 + (lane >> 3));
+  const bool along_cut = ((g.C - 1) / 64) * 64 + along_piece * 8 >= static_cast<uint32_t>(g.C);
+  const __bf16 *xbase, *rbase;  // the tile's first element
+  Rsrc xr, xr2, rr;
+  uint32_t xoff[LX], roff[LR];
+  int x_stages = 0, r_stages = 0, x_left = 0, r_left = 0;
+  uint32_t x_bytes = 0, r_bytes = 0;  // across: bytes of a row, and (_cols) before the tile's first element
+  uint32_t x_cols = 0, r_cols = 0;
+  const auto across_off = [&](int i, int width, uint32_t row_bytes, int valid) -> uint32_t {
+    const uint32_t k = (i * NW + wave) * (512 / width) + lane / (width / 8);
+    const uint32_t piece = (lane % (width / 8)) ^ across_swizzle(k);
+    return static_cast<int>(piece * 8) < valid ? k * row_bytes + piece * 16 : kNone;
+  };
+  const auto open_x = [&]() {
+    x_stages = stages_of(at);
+    const int valid = min(O - at.n0, BO);
+    if constexpr (kXAlong) {
+      const __bf16* we = g.x + (static_cast<size_t>(at.e) * (kPair ? 2 * O : O) + at.n0) * g.C;
+      const uint32_t bytes = static_cast<uint32_t>(g.C) * 2;
+      xr = make_rsrc(uniform(we), valid * bytes);
+      if constexpr (kPair) xr2 = make_rsrc(uniform(we + static_cast<size_t>(O) * g.C), valid * bytes);
+#pragma unroll
+      for (int i = 0; i < LX; ++i) {
+        const int r = ((kPair ? i % (LX / 2) : i) * NW + wave) * 8 + (lane >> 3);
+        xoff[i] = r < valid ? r * bytes + along_piece * 16 : kNone;
+      }
+    } else {
+      x_bytes = static_cast<uint32_t>(O) * 2;
+      x_cols = at.n0 * 2;
+      x_left = KIND == kWeights ? at.count : g.C;
+      xbase = uniform(g.x + (KIND == kWeights ? static_cast<size_t>(at.first) : static_cast<size_t>(at.e) * g.C) * O + at.n0);
+#pragma unroll
+      for (int i = 0; i < LX; ++i) xoff[i] = across_off(i, BN, x_bytes, valid);
+    }
+  };
+  const auto open_r = [&]() {
+    r_stages = stages_of(at);
+    const int valid = rows_in(at);
+    if constexpr (kRAlong) {
+      const uint32_t bytes = static_cast<uint32_t>(g.C) * 2;
+      rr = make_rsrc(uniform(g.r + (static_cast<size_t>(at.first) + at.m0) * g.C), valid * bytes);
+#pragma unroll
+      for (int i = 0; i < LR; ++i) {
+        const int r = (i * NW + wave) * 8 + (lane >> 3);
+        roff[i] = r < valid ? r * bytes + along_piece * 16 : kNone;
+      }
+    } else {
+      r_bytes = static_cast<uint32_t>(g.M) * 2;
+      r_cols = at.m0 * 2;
+      r_left = at.count;
+      rbase = uniform(g.r + static_cast<size_t>(at.first) * g.M + at.m0);
+#pragma unroll
+      for (int i = 0; i < LR; ++i) roff[i] = across_off(i, BM, r_bytes, valid);
+    }
+  };
+  const auto copy_x = [&](int s, bool none, uint8_t* buf) {
+    none = none || s >= x_stages;
+    if constexpr (kXAlong) {
+      const uint32_t gone = none || (s == x_stages - 1 && along_cut) ? kNone : 0;
+#pragma unroll
+      for (int i = 0; i < LX; ++i)
+        copy_piece<ONCE>(kPair && i >= LX / 2 ? xr2 : xr, buf + (i * NW + wave) * 1024, xoff[i] | gone, s * 128);
+    } else {
+      const int rows = none ? 0 : min(x_left - s * 64, 64);
+      const Rsrc src = make_rsrc(xbase + static_cast<size_t>(none ? 0 : s) * 64 * O, rows > 0 ? rows * x_bytes - x_cols : 0);
+#pragma unroll
+      for (int i = 0; i < LX; ++i) copy_piece<ONCE>(src, buf + (i * NW + wave) * 1024, xoff[i], 0);
+    }
+  };
+  const auto copy_r = [&](int s, bool none, uint8_t* buf) {
+    none = none || s >= r_stages;
+    if constexpr (kRAlong) {
+      const uint32_t gone = none || (s == r_stages - 1 && along_cut) ? kNone : 0;
+#pragma unroll
+      for (int i = 0; i < LR; ++i) copy16(rr, buf + (i * NW + wave) * 1024, roff[i] | gone, s * 128);
+    } else {
+      const int rows = none ? 0 : min(r_left - s * 64, 64);
+      const Rsrc src = make_rsrc(rbase + static_cast<size_t>(none ? 0 : s) * 64 * g.M, rows > 0 ? rows * r_bytes - r_cols : 0);
+#pragma unroll
+      for (int i = 0; i < LR; ++i) copy16(src, buf + (i * NW + wave) * 1024, roff[i], 0);
+    }
+  };
+
+  // ---- fragments ----
+  const auto x_frag = [&](int i) {  // the wave's fragment i of X, in the tile
+    if (!kPair) return wn * TN + i * 32;
+    return i < FN / 2 ? wn * (TN / 2) + i * 32 : BO + wn * (TN / 2) + (i - FN / 2) * 32;
+  };
+  const auto r_frag = [&](int j) { return (j * WM + wm) * 32; };  // in turn, so that short tiles keep all waves busy
+  // Where this lane reads: along, of fragment 0 by 16-element step; across, of
+  // step 0 by fragment.  (Opaque to the compiler: it would split them into sums of
+  // many terms, at the end of which it loses which buffer an address is in and waits
+  // for every copy.)
+  uint32_t xa[kXAlong ? 4 : FN], ra[kRAlong ? 4 : FM];
+  const auto lane_along = [&](int row, int ks) {
+    uint32_t v = (row + col) * 128 + ((ks * 2 + half) ^ along_swizzle(col)) * 16;
+    asm volatile("" : "+v"(v));
+    return v;
+  };
+  const auto lane_across = [&](int row, int width) {
+    const int j = lane & 15, b = (lane >> 4) & 1;
+    const uint32_t piece = (row / 8 + 2 * b + ((j & 3) >> 1)) ^ across_swizzle(j >> 2);
+    uint32_t v = (8 * half + (j >> 2)) * width * 2 + piece * 16 + (j & 1) * 8;
+    asm volatile("" : "+v"(v));
+    return v;
+  };
+  static_for<0, kXAlong ? 4 : FN>([&](auto ic) {
+    constexpr int i = decltype(ic)::value;
+    xa[i] = kXAlong ? lane_along(x_frag(0), i) : lane_across(x_frag(i), BN);
+  });
+  static_for<0, kRAlong ? 4 : FM>([&](auto jc) {
+    constexpr int j = decltype(jc)::value;
+    ra[j] = kRAlong ? lane_along(r_frag(0), j) : lane_across(r_frag(j), BM);
+  });
+  const auto along = [&](const uint8_t* p) { return *reinterpret_cast<const bf16x8*>(p); };
+  const auto across = [&](const uint8_t* p, int width) {
+    typedef __attribute__((address_space(3))) s16x4 Lds;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)(p + 4 * width * 2));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  bf16x8 xv[2][FN], rv[2][FM];
+  const auto read = [&](int set, int ks, const uint8_t* xb, const uint8_t* rb) {
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      const int row = x_frag(i) - x_frag(0);  // a constant
+      xv[set][i] = kXAlong ? along(xb + xa[kXAlong ? ks : 0] + row * 128) : across(xb + xa[kXAlong ? 0 : i] + ks * 32 * BN, BN);
+    }
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      const int row = r_frag(j) - r_frag(0);
+      rv[set][j] = kRAlong ? along(rb + ra[kRAlong ? ks : 0] + row * 128) : across(rb + ra[kRAlong ? 0 : j] + ks * 32 * BM, BM);
+    }
+  };
+  f32x16 acc[FN][FM];
+  const auto multiply = [&](int set) {
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xv[set][i], rv[set][j], acc[i][j], 0, 0, 0);
+  };
+  // One product, then its share of the next fragments' reads and of the copies,
+  // and so on: copies issued together would keep the wave from its products.
+  constexpr int kReads = FN * (kXAlong ? 1 : 2) + FM * (kRAlong ? 1 : 2), kMul = FN * FM;
+  const auto interleave = [&](auto copies) {
+    constexpr int kCopies = decltype(copies)::value;
+    static_for<0, kMul>([&](auto ic) {
+      constexpr int i = decltype(ic)::value;
+      constexpr int reads = kReads * (i + 1) / kMul - kReads * i / kMul, some = kCopies * (i + 1) / kMul - kCopies * i / kMul;
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
+      if constexpr (some > 0) __builtin_amdgcn_sched_group_barrier(0x10, some, 0);
+    });
+  };
+
+  open_tile();
+  open_x();
+  open_r();
+  // In the loop R of stage st + RS follows stage st, and X of stage st + XS - 1
+  // goes before its end, so that behind both operands of the next stage there are
+  // kAhead copies under way.
+  constexpr int kAhead = XS == RS ? (RS - 2) * (LX + LR) : (RS - 1) * LX + (RS - 2) * LR;
+  static_for<0, RS>([&](auto qc) {
+    constexpr int q = decltype(qc)::value;
+    if constexpr (q < XS - 1) copy_x(q, false, x_buf(qc));
+    copy_r(q, false, r_buf(qc));
+    asm volatile("" ::: "memory");
+  });
+  wait_copies<(XS - 2) * LX + (RS - 1) * LR>();
+  read(0, 0, x0, r0);
+  for (;;) {
+    const Place c = at;  // the tile being multiplied
+    const int c_rows = rows_in(c), c_stages = stages_of(c);
+    // its stages, and none or more without products, so that each tile starts with the same buffers
+    const int c_all = max((c_stages + kRing - 1) / kRing, 1) * kRing;
+    const bool live = wm * 32 < c_rows;  // else this wave's rows are all past the end
+    bool last = false;
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    const auto stage = [&](int st, auto pc) {
+      constexpr int P = decltype(pc)::value;
+      const uint8_t *xb = x_buf(pc), *rb = r_buf(pc);
+      constexpr std::integral_constant<int, P + 1> after{};
+      if (st + RS == c_all) {  // from here on R's copies are the next tile's, and X's with it or a stage later
+        tile += step;
+        last = tile >= end;
+        if (!last) {
+          open_tile();
+          open_r();
+        }
+      }
+      if (st + XS - 1 == c_all && !last) open_x();
+      const int sx = st + XS - 1 >= c_all ? st + XS - 1 - c_all : st + XS - 1;  // the stages to copy
+      const int sr = st + RS >= c_all ? st + RS - c_all : st + RS;
+      const bool no_x = last && st + XS - 1 >= c_all, no_r = last && st + RS >= c_all;
+      __builtin_amdgcn_sched_barrier(0);
+      copy_x(sx, no_x, x_buf(std::integral_constant<int, P + XS - 1>{}));
+      read(1, 1, xb, rb);
+      multiply(0);
+      interleave(std::integral_constant<int, LX>{});
+      __builtin_amdgcn_sched_barrier(0);
+      read(0, 2, xb, rb);
+      multiply(1);
+      interleave(std::integral_constant<int, 0>{});
+      __builtin_amdgcn_sched_barrier(0);
+      read(1, 3, xb, rb);
+      multiply(0);
+      interleave(std::integral_constant<int, 0>{});
+      __builtin_amdgcn_sched_barrier(0);
+      // the next stage has arrived, and this one's buffers are read
+      wait_copies<kAhead>();
+      __builtin_amdgcn_sched_barrier(0);
+      copy_r(sr, no_r, r_buf(pc));
+      read(0, 0, x_buf(after), r_buf(after));
+      multiply(1);
+      interleave(std::integral_constant<int, LR>{});
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");  // the copies' order stays: the wait above counts on it
+    };
+    for (int first = 0; first < c_all; first += kRing)
+      static_for<0, kRing>([&](auto pc) { stage(first + decltype(pc)::value, pc); });
+
+    // ---- the result ----
+    // A fragment goes through LDS (the last stage's X buffer, where the next copy of
+    // X goes, behind the barrier below), so that four lanes hold 32 channels of a
+    // row and store 64 bytes (from the accumulators' layout it would be 8).
+    uint8_t* const yb = x_buf(std::integral_constant<int, XS - 1>{}) + wave * 4096;
+    const auto y_place = [](uint32_t row, uint32_t piece) { return row * 128 + ((piece ^ (row & 7)) * 16); };
+    const auto emit = [&](const f32x16& v, int j, int n, auto&& store) {  // store(row, channel, eight values)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4*>(yb + y_place(col, 2 * q + half)) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = h * 16 + (lane >> 2), q = (lane & 3) * 2;
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(yb + y_place(row, q));
+        const f32x4 hi = *reinterpret_cast<const f32x4*>(yb + y_place(row, q + 1));
+        const int m = r_frag(j) + row, ch = c.n0 + n + q * 4;
+        if (m < c_rows && ch < O) store(m, ch, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      }
+      asm volatile("" ::: "memory");
+    };
+    const auto put = [](__bf16* to, const f32x8& v) {
+      *reinterpret_cast<bf16x8*>(to) = __builtin_convertvector(v, bf16x8);
+    };
+    const auto get = [](const __bf16* from) {
+      return __builtin_convertvector(*reinterpret_cast<const bf16x8*>(from), f32x8);
+    };
+    const size_t row0 = KIND == kWeights ? static_cast<size_t>(c.e) * g.M + c.m0 : static_cast<size_t>(c.first) + c.m0;
+    if (live && !(KIND == kWeights && g.add && c_stages == 0)) {
+#pragma unroll
+      for (int j = 0; j < FM; ++j) {
+        if (r_frag(j) >= c_rows) continue;
+        if constexpr (KIND == kForward) {
+#pragma unroll
+          for (int i = 0; i < (kPair ? FN / 2 : FN); ++i) {
+            const int n = x_frag(i);  // the fragment's first channel in the tile
+            f32x16 a = acc[i][j];
+            if (g.bias != nullptr) {
+              const __bf16* be = g.bias + static_cast<size_t>(c.e) * (kPair ? 2 * O : O) + c.n0;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int ch = min(n + 8 * q + 4 * half, O - c.n0 - 4);
+                const bf16x4 b = *reinterpret_cast<const bf16x4*>(be + ch);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) a[4 * q + v] += static_cast<float>(b[v]);
+              }
+            }
+            if constexpr (kPair) {
+              f32x16 u = acc[i + FN / 2][j];
+              if (g.bias != nullptr) {
+                const __bf16* be = g.bias + static_cast<size_t>(c.e) * 2 * O + O + c.n0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const int ch = min(n + 8 * q + 4 * half, O - c.n0 - 4);
+                  const bf16x4 b = *reinterpret_cast<const bf16x4*>(be + ch);
+#pragma unroll
+                  for (int v = 0; v < 4; ++v) u[4 * q + v] += static_cast<float>(b[v]);
+                }
+              }
+              if (g.p != nullptr) {
+                emit(a, j, n, [&](int m, int ch, const f32x8& v) { put(g.p + (row0 + m) * 2 * O + ch, v); });
+                emit(u, j, n, [&](int m, int ch, const f32x8& v) { put(g.p + (row0 + m) * 2 * O + O + ch, v); });
+              }
+#pragma unroll
+              for (int v = 0; v < 16; ++v) a[v] = silu_times(a[v], u[v]);
+            }
+            __bf16* y = static_cast<__bf16*>(g.y);
+            if (g.residual != nullptr)
+              emit(a, j, n, [&](int m, int ch, const f32x8& v) {
+                put(y + (row0 + m) * O + ch, v + get(g.residual + (row0 + m) * O + ch));
+              });
+            else
+              emit(a, j, n, [&](int m, int ch, const f32x8& v) { put(y + (row0 + m) * O + ch, v); });
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < FN; ++i) {
+            const int n = x_frag(i);
+            if constexpr (KIND == kRows && GATED) {
+              emit(acc[i][j], j, n, [&](int m, int ch, const f32x8& d) {
+                const size_t at = (row0 + m) * 2 * O + ch;
+                const f32x8 gv = get(g.p + at), uv = get(g.p + at + O);
+                f32x8 dg, du;
+#pragma unroll
+                for (int v = 0; v < 8; ++v) {
+                  const Gate k = gate(gv[v]);
+                  dg[v] = (d[v] * k.s1) * (uv[v] * k.s2) * (1.0f + gv[v] * k.n);
+                  du[v] = (d[v] * k.s1) * (gv[v] * k.s2);
+                }
+                put(static_cast<__bf16*>(g.y) + at, dg);
+                put(static_cast<__bf16*>(g.y) + at + O, du);
+              });
+            } else {
+              emit(acc[i][j], j, n, [&](int m, int ch, f32x8 v) {
+                T* to = static_cast<T*>(g.y) + (row0 + m) * O + ch;
+                if constexpr (std::is_same<T, float>::value) {
+                  f32x4* q = reinterpret_cast<f32x4*>(to);
+                  if (KIND == kWeights && g.add) v += __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7);
+                  q[0] = f32x4{v[0], v[1], v[2], v[3]};
+                  q[1] = f32x4{v[4], v[5], v[6], v[7]};
+                } else {
+                  if (KIND == kWeights && g.add) v += get(to);
+                  put(to, v);
+                }
+              });
+            }
+          }
+        }
+      }
+    }
+    if (last) break;
+    wait_reads();  // every wave's fragments have left LDS
+  }
+  __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0) lgkmcnt(0): no copy outlives the workgroup's LDS
+}
+
+template <typename Kernel>
+hipError_t launch_linear(Kernel kernel, int threads, int per_cu, const LinearArgs& g, hipStream_t stream) {
+  const int grid = max(device_cu_count() / 8, 1) * 8 * per_cu;
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), 0, stream, g);
+  return hipGetLastError();
+}
+template <Kind KIND, bool GATED, typename T, int BM, int BN, int WM, int WN, int XS, int RS, int PER, bool ONCE = false>
+hipError_t launch_tiles(const LinearArgs& g, hipStream_t stream) {
+  return launch_linear(linear_tiled<KIND, GATED, T, BM, BN, WM, WN, XS, RS, PER, ONCE>, WM * WN * kWave, PER, g, stream);
+}
+
+// What the choice of a tile goes by.  The rows of each expert are on the device;
+// the host knows their number, and for the padded layout no more than the
+// capacity, which stands for some 64 rows at most.
+struct LinearShape {
+  int64_t rows, hit;  // and experts that have any, at most
+  int64_t avg;        // rows of an expert
+  int64_t cus;
+  // Tiles of bm rows and bo of o channels fill the chip, or nearly.
+  bool fill(int bm, int o, int bo) const {
+    const int64_t row_tiles = max(hit, (rows + bm - 1) / bm);
+    return row_tiles * ((o + bo - 1) / bo) * 8 >= 7 * cus;
+  }
+};
+inline LinearShape linear_shape(const LinearArgs& g) {
+  const int64_t each = g.capacity > 0 ? min(g.capacity, 64) : g.num_rows / g.E;
+  const int64_t rows = g.capacity > 0 ? each * g.E : g.num_rows;
+  return LinearShape{rows, min(static_cast<int64_t>(g.E), rows), each, max(device_cu_count(), 1)};
+}
+
+inline const __bf16* b16(const uint16_t* p) { return reinterpret_cast<const __bf16*>(p); }
+inline __bf16* b16(uint16_t* p) { return reinterpret_cast<__bf16*>(p); }
+
+}  // namespace ep
