@@ -828,7 +828,7 @@ def expert_product(a, a_scale, w, w_scale, handle, activation=EP_ACT_NONE, strea
 def _flat(name, t):
     if t.dim() < 2 or not t.is_contiguous():  # (a copy made here would be on the current stream, not on ``stream``)
         raise ValueError("%s must be contiguous rows" % name)
-    return t.view(-1, t.shape[-1])
+    return t if t.dim() == 2 else t.view(-1, t.shape[-1])  # (a view costs the host a us)
 
 
 def _expert_rows(handle):

@@ -118,7 +118,10 @@ hipError_t launch(const LinearArgs& g, hipStream_t stream) {
   constexpr Kind F = kForward;
   const LinearShape s = linear_shape(g);
   const auto fill = [&](int bm, int bn) { return s.fill(bm, g.O, GATED ? bn / 2 : bn); };
-  if (s.avg > 170 && fill(256, 256)) return launch_tiles<F, GATED, __bf16, 256, 256, 2, 4, 3, 2, 1>(g, stream);
+  if (s.avg > 170 && fill(256, 256)) {
+    if (s.avg > 2048) return launch_tiles<F, GATED, __bf16, 256, 256, 4, 2, 2, 2, 1>(g, stream);
+    return launch_tiles<F, GATED, __bf16, 256, 256, 4, 2, 3, 2, 1>(g, stream);
+  }
   if (s.avg > 100 && fill(192, 256)) return launch_tiles<F, GATED, __bf16, 192, 256, 2, 4, 3, 2, 1>(g, stream);
   if (s.avg > 32 && fill(128, 256)) {
     if (s.avg <= 100) return launch_tiles<F, GATED, __bf16, 128, 256, 2, 4, 3, 3, 1, true>(g, stream);
@@ -140,7 +143,7 @@ hipError_t launch_expert_linear(const uint16_t* a, const uint16_t* w, const uint
                                 const int32_t* expert_rows, int32_t num_rows, int32_t E, int32_t capacity, int32_t H,
                                 int32_t N, bool gated, uint16_t* p, uint16_t* y, hipStream_t stream) {
   const LinearArgs g{b16(w), b16(a), b16(bias), b16(residual), expert_rows, num_rows, E, capacity, H,
-                     gated ? N / 2 : N, 0, false, b16(p), y};
+                     gated ? N / 2 : N, 0, false, b16(p), y, nullptr};
   return gated ? launch<true>(g, stream) : launch<false>(g, stream);
 }
 

@@ -46,6 +46,7 @@ struct LinearArgs {
   bool add;   // kWeights: add to what is there
   __bf16* p;  // kForward gated: out or null; kRows gated: in, may be y
   void* y;
+  void* sums;  // kWeights: sums of r's columns (the biases' gradient) out, or null
 };
 
 // Rows of expert e; without expert_rows every row is expert 0's.
@@ -129,6 +130,7 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
   static_assert(!kPair || (FN % 2 == 0 && LX % 2 == 0), "a wave holds, and copies, both halves of its channels");
   static_assert((kXAlong || BN >= 128) && (kRAlong || BM >= 128), "across_swizzle permutes 16 pieces");
   static_assert(BN * 128 >= NW * 4096, "y's fragments");
+  static_assert(KIND != kWeights || NW * kWave >= BM, "a lane for each column's sum");
   static_assert(XS == RS || XS == RS + 1, "the order of the copies");
   constexpr int kRing = XS == RS ? XS : XS * RS;  // stages after which the buffers repeat
   static_assert(XS <= 6 && RS <= 6, "buffers");
@@ -173,12 +175,52 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
   const int E = g.E;
 
   // ---- tiles ----
-  // kForward, kRows: the row tiles of each expert times nt; they go in eight
-  // runs, one per XCD (workgroups go to the XCDs in turn), so that neighbouring
-  // tiles, which share weights or rows, meet in one L2.  Each wavefront finds its
-  // first one from sums over E / 64 experts a lane, and walks on from there.
-  // kWeights: every expert has the same tiles, but sums of its own length; they
-  // are dealt out in turns of one a workgroup, each XCD's next to one another.
+  // Neighbouring tiles share weights or rows, and are to meet in one XCD's L2
+  // (workgroups go to the XCDs in turn).  They are dealt out in turns of one a
+  // workgroup, 32 of an XCD next to one another; or, where few rows an expert make
+  // all of them streams of weights, in eight runs, one per XCD (128 tokens, 8 of 256
+  // experts: 2191 against 2227 us; but 4096 tokens with popular experts, whose
+  // tiles differ: 4028 against 3825).
+  // kForward, kRows: the row tiles of each expert times nt; each wavefront finds
+  // its first one from sums over E / 64 experts a lane, and walks on from there.
+  constexpr bool kRuns = KIND != kWeights && BM <= 128;
+  // kWeights: every expert has the same tiles, but sums of its own length.  The
+  // experts go by falling length, and every other turn is dealt backwards, so that
+  // no workgroup is left with a long sum at the end (32 experts, popular ones: 960
+  // against 1200 us).  order: this lane's experts in that order, the 64 i-th on,
+  // two in a register.
+  uint32_t order[KIND == kWeights ? kMaxExperts / kWave / 2 : 1];
+  if constexpr (KIND == kWeights) {
+    int32_t* const counts = reinterpret_cast<int32_t*>(x0);
+    uint16_t* const sorted = reinterpret_cast<uint16_t*>(x0 + kMaxExperts * 4);
+    static_assert(BN * 128 >= kMaxExperts * 6, "the experts' order");
+    for (int e = tid; e < E; e += NW * kWave) {
+      int first, count;
+      span_of(g.expert_rows, e, g.capacity, g.num_rows, first, count);
+      counts[e] = count;
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += NW * kWave) {
+      const int mine = counts[e];
+      int rank = 0;
+      for (int o = 0; o < E; ++o) rank += counts[o] > mine || (counts[o] == mine && o < e);
+      sorted[rank] = static_cast<uint16_t>(e);
+    }
+    __syncthreads();
+    static_for<0, kMaxExperts / kWave / 2>([&](auto ic) {
+      const int lo = 128 * decltype(ic)::value + lane, hi = lo + 64;
+      order[decltype(ic)::value] = (lo < E ? sorted[lo] : 0) | static_cast<uint32_t>(hi < E ? sorted[hi] : 0) << 16;
+    });
+    __syncthreads();
+  }
+  const auto expert_at = [&](uint32_t rank) -> int {
+    uint32_t pair = order[0];
+    static_for<1, KIND == kWeights ? kMaxExperts / kWave / 2 : 1>([&](auto ic) {
+      if (rank / 128 == decltype(ic)::value) pair = order[decltype(ic)::value];
+    });
+    pair = __builtin_amdgcn_readlane(pair, rank % 64);
+    return rank & 64 ? pair >> 16 : pair & 0xFFFF;
+  };
   const auto row_tiles = [&](int e) -> uint32_t {
     int first, count;
     span_of(g.expert_rows, e, g.capacity, g.num_rows, first, count);
@@ -213,10 +255,16 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
     // (2^30 tiles at most: rows that lie apart make far fewer)
     const uint64_t all = static_cast<uint64_t>(__shfl(upto, kWave - 1)) * nt;
     const uint32_t tiles = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(min(all, static_cast<uint64_t>(0x40000000))));
-    const uint32_t run = (tiles + 7) / 8;
-    step = gridDim.x / 8;
-    end = min((blockIdx.x & 7) * run + run, tiles);
-    tile = (blockIdx.x & 7) * run + blockIdx.x / 8;
+    if constexpr (kRuns) {
+      const uint32_t run = (tiles + 7) / 8;
+      step = gridDim.x / 8;
+      end = min((blockIdx.x & 7) * run + run, tiles);
+      tile = (blockIdx.x & 7) * run + blockIdx.x / 8;
+    } else {
+      end = tiles;
+      step = gridDim.x;
+      tile = (blockIdx.x & 7) * (gridDim.x / 8) + blockIdx.x / 8;
+    }
     if (tile >= end) return;
     // the first lane that ends beyond this tile's row tile holds its expert
     const int at = __builtin_ctzll(wave_ballot(upto > static_cast<int64_t>(tile / nt)));
@@ -238,10 +286,12 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
   };
   const auto open_tile = [&]() {
     if constexpr (KIND == kWeights) {
-      const uint32_t each = te * nt;
-      at.e = tile / each;
-      const uint32_t local = tile - at.e * each;
-      place(local);
+      const uint32_t each = te * nt, turn = tile / gridDim.x;
+      // (not the last, incomplete turn)
+      const uint32_t q = (turn & 1) != 0 && (turn + 1) * gridDim.x <= end ? (2 * turn + 1) * gridDim.x - 1 - tile : tile;
+      const uint32_t rank = q / each;
+      at.e = expert_at(rank);
+      place(q - rank * each);
     } else {
       const uint32_t q = tile / nt;
       while (q >= static_cast<uint64_t>(before + te)) {  // ends at the expert of tile q
@@ -440,6 +490,16 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
     // its stages, and none or more without products, so that each tile starts with the same buffers
     const int c_all = max((c_stages + kRing - 1) / kRing, 1) * kRing;
     const bool live = wm * 32 < c_rows;  // else this wave's rows are all past the end
+    // The tiles of the first channels sum R's columns as well, from the stages in
+    // LDS: each lane eight columns of every kAtOnce-th row.
+    constexpr int kPieces = BM / 8, kAtOnce = NW * kWave / kPieces;
+    const bool c_sums = KIND == kWeights && g.sums != nullptr && c.n0 == 0;
+    f32x8 columns = {0, 0, 0, 0, 0, 0, 0, 0};
+    const auto add_columns = [&](const uint8_t* rb) {
+#pragma unroll
+      for (int i = 0; i < 64 / kAtOnce; ++i)
+        columns += __builtin_convertvector(*reinterpret_cast<const bf16x8*>(rb + (tid * 16 + i * NW * 1024)), f32x8);
+    };
     bool last = false;
 #pragma unroll
     for (int i = 0; i < FN; ++i)
@@ -477,6 +537,9 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
       multiply(0);
       interleave(std::integral_constant<int, 0>{});
       __builtin_amdgcn_sched_barrier(0);
+      if constexpr (KIND == kWeights) {
+        if (c_sums) add_columns(rb);
+      }
       // the next stage has arrived, and this one's buffers are read
       wait_copies<kAhead>();
       __builtin_amdgcn_sched_barrier(0);
@@ -518,6 +581,24 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
       return __builtin_convertvector(*reinterpret_cast<const bf16x8*>(from), f32x8);
     };
     const size_t row0 = KIND == kWeights ? static_cast<size_t>(c.e) * g.M + c.m0 : static_cast<size_t>(c.first) + c.m0;
+    if constexpr (KIND == kWeights) {
+      if (c_sums) {
+        float* const part = reinterpret_cast<float*>(x_buf(std::integral_constant<int, XS - 1>{}));
+        static_assert(BN * 128 >= kAtOnce * BM * 4, "the column sums");
+        const int k = tid / kPieces, n = ((tid % kPieces) ^ across_swizzle(k)) * 8;  // (a row's pieces lie permuted)
+        f32x4* const mine = reinterpret_cast<f32x4*>(part + (k * BM + n));
+        mine[0] = f32x4{columns[0], columns[1], columns[2], columns[3]};
+        mine[1] = f32x4{columns[4], columns[5], columns[6], columns[7]};
+        wait_reads();
+        if (tid < c_rows && !(g.add && c_stages == 0)) {
+          float sum = 0.0f;
+          for (int i = 0; i < kAtOnce; ++i) sum += part[i * BM + tid];
+          T* const to = static_cast<T*>(g.sums) + (row0 + tid);
+          *to = static_cast<T>(g.add ? sum + static_cast<float>(*to) : sum);
+        }
+        wait_reads();
+      }
+    }
     if (live && !(KIND == kWeights && g.add && c_stages == 0)) {
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
