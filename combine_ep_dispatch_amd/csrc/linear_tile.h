@@ -49,6 +49,19 @@ struct LinearArgs {
   void* sums;  // kWeights: sums of r's columns (the biases' gradient) out, or null
 };
 
+// A value that is the same in every lane, kept where the compiler knows it (a
+// branch on anything else is taken for one that lanes take apart, and then the
+// copies of both its sides are waited for).
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+template <typename T>
+__device__ __forceinline__ T* uniform(T* p) {
+  return reinterpret_cast<T*>(uniform(reinterpret_cast<int64_t>(p)));
+}
+
 // Rows of expert e; without expert_rows every row is expert 0's.
 __device__ __forceinline__ void span_of(const int32_t* __restrict__ expert_rows, int e, int capacity, int num_rows,
                                         int& first, int& count) {
@@ -57,6 +70,24 @@ __device__ __forceinline__ void span_of(const int32_t* __restrict__ expert_rows,
     count = num_rows;
   } else {
     rows_of(expert_rows, e, capacity, num_rows, first, count);
+  }
+}
+
+// The same for an expert that is one for the wavefront, through the scalar cache:
+// a load that the copies under way are not waited for with.
+__device__ __forceinline__ void span_of_one(const int32_t* expert_rows, int e, int capacity, int num_rows, int& first,
+                                            int& count) {
+  typedef __attribute__((address_space(4))) const int32_t Constant;
+  Constant* rows = (Constant*)(uintptr_t)uniform(expert_rows);
+  e = __builtin_amdgcn_readfirstlane(e);
+  if (expert_rows == nullptr) {
+    first = 0;
+    count = num_rows;
+  } else if (capacity > 0) {
+    first = e * capacity;
+    count = min(max(rows[e], 0), capacity);
+  } else {
+    span_rows(rows[e], rows[e + 1], num_rows, first, count);
   }
 }
 
@@ -92,19 +123,6 @@ __device__ __forceinline__ void wait_copies() {
 __device__ __forceinline__ uint32_t along_swizzle(uint32_t row) { return (row & 7) ^ ((row >> 3) & 1); }
 // Pairs of pieces of the rows that a transposing load reads together.
 __device__ __forceinline__ uint32_t across_swizzle(uint32_t k) { return ((k & 3) | (k & 1) << 2) * 2; }
-
-// A value that is the same in every lane, kept where the compiler knows it (a
-// branch on anything else is taken for one that lanes take apart, and then the
-// copies of both its sides are waited for).
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
-  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
-  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
-}
-template <typename T>
-__device__ __forceinline__ T* uniform(T* p) {
-  return reinterpret_cast<T*>(uniform(reinterpret_cast<int64_t>(p)));
-}
 
 template <bool ONCE>
 __device__ __forceinline__ void copy_piece(Rsrc src, uint8_t* dst, uint32_t lane_off, uint32_t off) {
@@ -214,9 +232,9 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
     __syncthreads();
   }
   const auto expert_at = [&](uint32_t rank) -> int {
-    uint32_t pair = order[0];
-    static_for<1, KIND == kWeights ? kMaxExperts / kWave / 2 : 1>([&](auto ic) {
-      if (rank / 128 == decltype(ic)::value) pair = order[decltype(ic)::value];
+    uint32_t pair = 0;  // (added up: chosen from, the registers would go to scratch memory)
+    static_for<0, KIND == kWeights ? kMaxExperts / kWave / 2 : 1>([&](auto ic) {
+      pair |= rank / 128 == decltype(ic)::value ? order[decltype(ic)::value] : 0;
     });
     pair = __builtin_amdgcn_readlane(pair, rank % 64);
     return rank & 64 ? pair >> 16 : pair & 0xFFFF;
@@ -224,6 +242,11 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
   const auto row_tiles = [&](int e) -> uint32_t {
     int first, count;
     span_of(g.expert_rows, e, g.capacity, g.num_rows, first, count);
+    return (static_cast<uint32_t>(count) + BM - 1) / BM;
+  };
+  const auto row_tiles_of_one = [&](int e) -> uint32_t {
+    int first, count;
+    span_of_one(g.expert_rows, e, g.capacity, g.num_rows, first, count);
     return (static_cast<uint32_t>(count) + BM - 1) / BM;
   };
   uint32_t tile, end, step, te = 0;
@@ -270,7 +293,7 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
     const int at = __builtin_ctzll(wave_ballot(upto > static_cast<int64_t>(tile / nt)));
     before = uniform(__shfl(upto - mine, at));
     walk = __builtin_amdgcn_readfirstlane(at * per);
-    te = __builtin_amdgcn_readfirstlane(row_tiles(walk));
+    te = row_tiles_of_one(walk);
   }
 
   // ---- the tile whose stages are being copied ----
@@ -296,15 +319,13 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
       const uint32_t q = tile / nt;
       while (q >= static_cast<uint64_t>(before + te)) {  // ends at the expert of tile q
         before += te;
-        te = __builtin_amdgcn_readfirstlane(row_tiles(++walk));
+        te = row_tiles_of_one(++walk);
       }
       at.e = walk;
       const uint32_t local = tile - static_cast<uint32_t>(before) * nt;
       place(local);
     }
-    span_of(g.expert_rows, at.e, g.capacity, g.num_rows, at.first, at.count);
-    at.first = __builtin_amdgcn_readfirstlane(at.first);
-    at.count = __builtin_amdgcn_readfirstlane(at.count);
+    span_of_one(g.expert_rows, at.e, g.capacity, g.num_rows, at.first, at.count);
   };
   const auto stages_of = [&](const Place& t) { return ((KIND == kWeights ? t.count : g.C) + 63) / 64; };
   const auto rows_in = [&](const Place& t) { return min((KIND == kWeights ? g.M : t.count) - t.m0, BM); };
@@ -554,32 +575,6 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
       static_for<0, kRing>([&](auto pc) { stage(first + decltype(pc)::value, pc); });
 
     // ---- the result ----
-    // A fragment goes through LDS (the last stage's X buffer, where the next copy of
-    // X goes, behind the barrier below), so that four lanes hold 32 channels of a
-    // row and store 64 bytes (from the accumulators' layout it would be 8).
-    uint8_t* const yb = x_buf(std::integral_constant<int, XS - 1>{}) + wave * 4096;
-    const auto y_place = [](uint32_t row, uint32_t piece) { return row * 128 + ((piece ^ (row & 7)) * 16); };
-    const auto emit = [&](const f32x16& v, int j, int n, auto&& store) {  // store(row, channel, eight values)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<f32x4*>(yb + y_place(col, 2 * q + half)) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-      asm volatile("" ::: "memory");
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = h * 16 + (lane >> 2), q = (lane & 3) * 2;
-        const f32x4 lo = *reinterpret_cast<const f32x4*>(yb + y_place(row, q));
-        const f32x4 hi = *reinterpret_cast<const f32x4*>(yb + y_place(row, q + 1));
-        const int m = r_frag(j) + row, ch = c.n0 + n + q * 4;
-        if (m < c_rows && ch < O) store(m, ch, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-      }
-      asm volatile("" ::: "memory");
-    };
-    const auto put = [](__bf16* to, const f32x8& v) {
-      *reinterpret_cast<bf16x8*>(to) = __builtin_convertvector(v, bf16x8);
-    };
-    const auto get = [](const __bf16* from) {
-      return __builtin_convertvector(*reinterpret_cast<const bf16x8*>(from), f32x8);
-    };
     const size_t row0 = KIND == kWeights ? static_cast<size_t>(c.e) * g.M + c.m0 : static_cast<size_t>(c.first) + c.m0;
     if constexpr (KIND == kWeights) {
       if (c_sums) {
@@ -599,87 +594,147 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
         wait_reads();
       }
     }
-    if (live && !(KIND == kWeights && g.add && c_stages == 0)) {
+    // A fragment goes through LDS (the last stage's X buffer, where the next copy of
+    // X goes, behind the barrier below), so that four lanes hold 32 channels of a
+    // row and store 64 bytes (from the accumulators' layout it would be 8).  What a
+    // fragment needs from memory is read before the one before it is stored: a
+    // wait for loads is one for the stores ahead of them.  Rows and channels past the
+    // end are past the end of the buffer resources, where nothing is read or written.
+    uint8_t* const yb = x_buf(std::integral_constant<int, XS - 1>{}) + wave * 4096;
+    const auto y_place = [](uint32_t row, uint32_t piece) { return row * 128 + ((piece ^ (row & 7)) * 16); };
+    const auto turn = [&](const f32x16& v, f32x8(&out)[2]) {  // rows lane / 4 and 16 + lane / 4 of a fragment
 #pragma unroll
-      for (int j = 0; j < FM; ++j) {
-        if (r_frag(j) >= c_rows) continue;
-        if constexpr (KIND == kForward) {
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4*>(yb + y_place(col, 2 * q + half)) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      asm volatile("" ::: "memory");
 #pragma unroll
-          for (int i = 0; i < (kPair ? FN / 2 : FN); ++i) {
-            const int n = x_frag(i);  // the fragment's first channel in the tile
-            f32x16 a = acc[i][j];
-            if (g.bias != nullptr) {
-              const __bf16* be = g.bias + static_cast<size_t>(c.e) * (kPair ? 2 * O : O) + c.n0;
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t row = h * 16 + (lane >> 2), q = (lane & 3) * 2;
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(yb + y_place(row, q));
+        const f32x4 hi = *reinterpret_cast<const f32x4*>(yb + y_place(row, q + 1));
+        out[h] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      }
+      asm volatile("" ::: "memory");
+    };
+    constexpr bool kDouble = KIND == kRows && GATED;  // rows of 2 O channels
+    constexpr uint32_t kSize = sizeof(T);
+    const uint32_t y_bytes = (kDouble ? 2 : 1) * static_cast<uint32_t>(O) * kSize, p_bytes = 2 * static_cast<uint32_t>(O) * 2;
+    const Rsrc yr = make_rsrc(uniform(static_cast<T*>(g.y) + row0 * (kDouble ? 2 * O : O)), c_rows * y_bytes);
+    Rsrc pr = yr, resr = yr, br = yr;
+    if (kPair || kDouble) pr = make_rsrc(uniform(g.p + row0 * 2 * O), g.p != nullptr ? c_rows * p_bytes : 0);
+    if (KIND == kForward) {
+      resr = make_rsrc(uniform(g.residual + row0 * O), g.residual != nullptr ? c_rows * y_bytes : 0);
+      br = make_rsrc(uniform(g.bias + static_cast<size_t>(c.e) * (kPair ? 2 * O : O)), g.bias != nullptr ? (kPair ? 4 : 2) * O : 0);
+    }
+    const auto get = [](Rsrc from, uint32_t off) {
+      return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(from, off, 0, 0));
+    };
+    const auto put = [](Rsrc to, uint32_t off, const f32x8& v) {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, __builtin_convertvector(v, bf16x8)), to, off, 0, 0);
+    };
+    const auto wide = [](const bf16x8& v) { return __builtin_convertvector(v, f32x8); };
+    // Fragment f: rows f / kAcross, channels f % kAcross.
+    constexpr int kAcross = kPair ? FN / 2 : FN, kFragments = kAcross * FM;
+    const auto channel = [&](int f) -> uint32_t { return c.n0 + x_frag(f % kAcross) + (lane & 3) * 8; };
+    // its offset, for rows of so many bytes and elements of so many, of channel + more
+    const auto offset = [&](int f, int h, uint32_t bytes, uint32_t size, uint32_t more) -> uint32_t {
+      const uint32_t m = r_frag(f / kAcross) + h * 16 + (lane >> 2), n = channel(f);
+      return n < static_cast<uint32_t>(O) ? m * bytes + (n + more) * size : kNone;
+    };
+    bf16x8 bias[2][2], old[2][kDouble ? 4 : 2];
+    const bool adds = KIND == kWeights && g.add;
+    const auto fetch = [&](int f) {
+      const int b = f & 1;
+      if constexpr (KIND == kForward) {
+        const uint32_t n = channel(f);
+        if (g.bias != nullptr) {
+          bias[b][0] = get(br, n < static_cast<uint32_t>(O) ? n * 2 : kNone);
+          if constexpr (kPair) bias[b][1] = get(br, n < static_cast<uint32_t>(O) ? (n + O) * 2 : kNone);
+        }
+        if (g.residual != nullptr) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int ch = min(n + 8 * q + 4 * half, O - c.n0 - 4);
-                const bf16x4 b = *reinterpret_cast<const bf16x4*>(be + ch);
+          for (int h = 0; h < 2; ++h) old[b][h] = get(resr, offset(f, h, y_bytes, 2, 0));
+        }
+      } else if constexpr (kDouble) {
 #pragma unroll
-                for (int v = 0; v < 4; ++v) a[4 * q + v] += static_cast<float>(b[v]);
-              }
-            }
-            if constexpr (kPair) {
-              f32x16 u = acc[i + FN / 2][j];
-              if (g.bias != nullptr) {
-                const __bf16* be = g.bias + static_cast<size_t>(c.e) * 2 * O + O + c.n0;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const int ch = min(n + 8 * q + 4 * half, O - c.n0 - 4);
-                  const bf16x4 b = *reinterpret_cast<const bf16x4*>(be + ch);
-#pragma unroll
-                  for (int v = 0; v < 4; ++v) u[4 * q + v] += static_cast<float>(b[v]);
-                }
-              }
-              if (g.p != nullptr) {
-                emit(a, j, n, [&](int m, int ch, const f32x8& v) { put(g.p + (row0 + m) * 2 * O + ch, v); });
-                emit(u, j, n, [&](int m, int ch, const f32x8& v) { put(g.p + (row0 + m) * 2 * O + O + ch, v); });
-              }
-#pragma unroll
-              for (int v = 0; v < 16; ++v) a[v] = silu_times(a[v], u[v]);
-            }
-            __bf16* y = static_cast<__bf16*>(g.y);
-            if (g.residual != nullptr)
-              emit(a, j, n, [&](int m, int ch, const f32x8& v) {
-                put(y + (row0 + m) * O + ch, v + get(g.residual + (row0 + m) * O + ch));
-              });
-            else
-              emit(a, j, n, [&](int m, int ch, const f32x8& v) { put(y + (row0 + m) * O + ch, v); });
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < FN; ++i) {
-            const int n = x_frag(i);
-            if constexpr (KIND == kRows && GATED) {
-              emit(acc[i][j], j, n, [&](int m, int ch, const f32x8& d) {
-                const size_t at = (row0 + m) * 2 * O + ch;
-                const f32x8 gv = get(g.p + at), uv = get(g.p + at + O);
-                f32x8 dg, du;
-#pragma unroll
-                for (int v = 0; v < 8; ++v) {
-                  const Gate k = gate(gv[v]);
-                  dg[v] = (d[v] * k.s1) * (uv[v] * k.s2) * (1.0f + gv[v] * k.n);
-                  du[v] = (d[v] * k.s1) * (gv[v] * k.s2);
-                }
-                put(static_cast<__bf16*>(g.y) + at, dg);
-                put(static_cast<__bf16*>(g.y) + at + O, du);
-              });
-            } else {
-              emit(acc[i][j], j, n, [&](int m, int ch, f32x8 v) {
-                T* to = static_cast<T*>(g.y) + (row0 + m) * O + ch;
-                if constexpr (std::is_same<T, float>::value) {
-                  f32x4* q = reinterpret_cast<f32x4*>(to);
-                  if (KIND == kWeights && g.add) v += __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7);
-                  q[0] = f32x4{v[0], v[1], v[2], v[3]};
-                  q[1] = f32x4{v[4], v[5], v[6], v[7]};
-                } else {
-                  if (KIND == kWeights && g.add) v += get(to);
-                  put(to, v);
-                }
-              });
-            }
-          }
+        for (int h = 0; h < 2; ++h) {
+          old[b][2 * h] = get(pr, offset(f, h, p_bytes, 2, 0));
+          old[b][2 * h + 1] = get(pr, offset(f, h, p_bytes, 2, O));
         }
       }
+    };
+    const auto finish = [&](auto fc) {
+      constexpr int f = decltype(fc)::value, b = f & 1, i = f % kAcross, j = f / kAcross;
+      f32x8 v[2], u[2];
+      turn(acc[i][j], v);
+      if constexpr (kPair) turn(acc[i + FN / 2][j], u);
+      if constexpr (KIND == kForward) {
+        if (g.bias != nullptr) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            v[h] += wide(bias[b][0]);
+            if constexpr (kPair) u[h] += wide(bias[b][1]);
+          }
+        }
+        if constexpr (kPair) {
+          if (g.p != nullptr) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              put(pr, offset(f, h, p_bytes, 2, 0), v[h]);
+              put(pr, offset(f, h, p_bytes, 2, O), u[h]);
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[h][x] = silu_times(v[h][x], u[h][x]);
+        }
+        if (g.residual != nullptr) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) v[h] += wide(old[b][h]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) put(yr, offset(f, h, y_bytes, 2, 0), v[h]);
+      } else if constexpr (kDouble) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f32x8 gv = wide(old[b][2 * h]), uv = wide(old[b][2 * h + 1]);
+          f32x8 dg, du;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const Gate k = gate(gv[x]);
+            dg[x] = (v[h][x] * k.s1) * (uv[x] * k.s2) * (1.0f + gv[x] * k.n);
+            du[x] = (v[h][x] * k.s1) * (gv[x] * k.s2);
+          }
+          put(yr, offset(f, h, y_bytes, 2, 0), dg);
+          put(yr, offset(f, h, y_bytes, 2, O), du);
+        }
+      } else if constexpr (kSize == 4) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            f32x4 w = {v[h][4 * x], v[h][4 * x + 1], v[h][4 * x + 2], v[h][4 * x + 3]};
+            if (adds) w += __builtin_bit_cast(f32x4, get(yr, offset(f, h, y_bytes, 4, 4 * x)));
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), yr, offset(f, h, y_bytes, 4, 4 * x), 0, 0);
+          }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (adds) v[h] += wide(get(yr, offset(f, h, y_bytes, 2, 0)));
+          put(yr, offset(f, h, y_bytes, 2, 0), v[h]);
+        }
+      }
+    };
+    if (live && !(adds && c_stages == 0)) {
+      fetch(0);
+      static_while<0, kFragments>([&](auto fc) {
+        constexpr int f = decltype(fc)::value;
+        if (f % kAcross == 0 && r_frag(f / kAcross) >= c_rows) return false;  // (nor have those behind it)
+        if constexpr (f + 1 < kFragments) fetch(f + 1);
+        finish(fc);
+        return true;
+      });
     }
     if (last) break;
     wait_reads();  // every wave's fragments have left LDS
