@@ -544,6 +544,7 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
       const int sx = st + XS - 1 >= c_all ? st + XS - 1 - c_all : st + XS - 1;  // the stages to copy
       const int sr = st + RS >= c_all ? st + RS - c_all : st + RS;
       const bool no_x = last && st + XS - 1 >= c_all, no_r = last && st + RS >= c_all;
+      if (st < c_stages) {
       __builtin_amdgcn_sched_barrier(0);
       copy_x(sx, no_x, x_buf(std::integral_constant<int, P + XS - 1>{}));
       read(1, 1, xb, rb);
@@ -569,6 +570,13 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
       multiply(1);
       interleave(std::integral_constant<int, LR>{});
       __builtin_amdgcn_sched_barrier(0);
+      } else {  // (its wait for all copies, once a tile, spares the compiler's own in the stages above)
+        copy_x(sx, no_x, x_buf(std::integral_constant<int, P + XS - 1>{}));
+        wait_copies<kAhead>();
+        copy_r(sr, no_r, r_buf(pc));
+        read(0, 0, x_buf(after), r_buf(after));
+        __builtin_amdgcn_s_waitcnt(7 << 4 | 15 << 8);  // vmcnt(0)
+      }
       asm volatile("" ::: "memory");  // the copies' order stays: the wait above counts on it
     };
     for (int first = 0; first < c_all; first += kRing)
@@ -602,11 +610,14 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
     // end are past the end of the buffer resources, where nothing is read or written.
     uint8_t* const yb = x_buf(std::integral_constant<int, XS - 1>{}) + wave * 4096;
     const auto y_place = [](uint32_t row, uint32_t piece) { return row * 128 + ((piece ^ (row & 7)) * 16); };
-    const auto turn = [&](const f32x16& v, f32x8(&out)[2]) {  // rows lane / 4 and 16 + lane / 4 of a fragment
+    const auto lay = [&](const f32x16& v) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         *reinterpret_cast<f32x4*>(yb + y_place(col, 2 * q + half)) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
       asm volatile("" ::: "memory");
+    };
+    const auto turn = [&](const f32x16& v, f32x8(&out)[2]) {  // rows lane / 4 and 16 + lane / 4 of a fragment
+      lay(v);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t row = h * 16 + (lane >> 2), q = (lane & 3) * 2;
@@ -666,7 +677,8 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
     const auto finish = [&](auto fc) {
       constexpr int f = decltype(fc)::value, b = f & 1, i = f % kAcross, j = f / kAcross;
       f32x8 v[2], u[2];
-      turn(acc[i][j], v);
+      if constexpr (kSize == 4) lay(acc[i][j]);
+      else turn(acc[i][j], v);
       if constexpr (kPair) turn(acc[i + FN / 2][j], u);
       if constexpr (KIND == kForward) {
         if (g.bias != nullptr) {
@@ -711,13 +723,14 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
         }
       } else if constexpr (kSize == 4) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            f32x4 w = {v[h][4 * x], v[h][4 * x + 1], v[h][4 * x + 2], v[h][4 * x + 3]};
-            if (adds) w += __builtin_bit_cast(f32x4, get(yr, offset(f, h, y_bytes, 4, 4 * x)));
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), yr, offset(f, h, y_bytes, 4, 4 * x), 0, 0);
-          }
+        for (int h = 0; h < 4; ++h) {  // whole lines of 32 channels, eight rows at a time
+          const uint32_t row = h * 8 + (lane >> 3), m = r_frag(j) + row, n = c.n0 + x_frag(i) + (lane & 7) * 4;
+          const uint32_t at = n < static_cast<uint32_t>(O) ? m * y_bytes + n * 4 : kNone;
+          f32x4 w = *reinterpret_cast<const f32x4*>(yb + y_place(row, lane & 7));
+          if (adds) w += __builtin_bit_cast(f32x4, get(yr, at));
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), yr, at, 0, 0);
+        }
+        asm volatile("" ::: "memory");
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
