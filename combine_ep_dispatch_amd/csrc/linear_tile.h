@@ -250,7 +250,7 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
     return (static_cast<uint32_t>(count) + BM - 1) / BM;
   };
   uint32_t tile, end, step, te = 0;
-  int64_t before = 0;  // row tiles before expert `walk`
+  uint32_t before = 0;  // row tiles before expert `walk`
   int walk = 0;
   if constexpr (KIND == kWeights) {
     te = (g.M + BM - 1) / BM;
@@ -260,24 +260,27 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
     tile = (blockIdx.x & 7) * (gridDim.x / 8) + blockIdx.x / 8;
     if (tile >= end) return;
   } else {
-    int64_t mine = 0;
+    uint32_t mine = 0, upto = 0, total;
     const int per = (E + kWave - 1) / kWave;  // experts of a lane
-    for (int i = 0; i < per; i += 4) {
-      uint32_t n[4];  // (loaded for any lane, so that the four loads overlap)
+    if (g.expert_rows == nullptr) {
+      total = te = row_tiles_of_one(0);
+    } else {
+      for (int i = 0; i < per; i += 4) {
+        uint32_t n[4];  // (loaded for any lane, so that the four loads overlap)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) n[x] = row_tiles(min(lane * per + i + x, E - 1));
+        for (int x = 0; x < 4; ++x) n[x] = row_tiles(min(lane * per + i + x, E - 1));
 #pragma unroll
-      for (int x = 0; x < 4; ++x) mine += i + x < per && lane * per + i + x < E ? n[x] : 0;
+        for (int x = 0; x < 4; ++x) mine += i + x < per && lane * per + i + x < E ? n[x] : 0;
+      }
+      upto = wave_inclusive_scan(mine);
+      total = __builtin_amdgcn_readlane(upto, kWave - 1);
+      // Rows that lie apart are below 2^26 row tiles; where offsets out of order let
+      // experts share rows so often that the sums could pass 32 bits, nothing is done.
+      const uint32_t high = __builtin_amdgcn_readlane(wave_inclusive_scan(mine >> 16), kWave - 1);
+      if (high >= 1 << 14) return;
     }
-    int64_t upto = mine;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const int64_t o = __shfl_up(upto, d);
-      if (lane >= d) upto += o;
-    }
-    // (2^30 tiles at most: rows that lie apart make far fewer)
-    const uint64_t all = static_cast<uint64_t>(__shfl(upto, kWave - 1)) * nt;
-    const uint32_t tiles = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(min(all, static_cast<uint64_t>(0x40000000))));
+    // (2^30 tiles at most)
+    const uint32_t tiles = static_cast<uint32_t>(min(static_cast<uint64_t>(total) * nt, static_cast<uint64_t>(0x40000000)));
     if constexpr (kRuns) {
       const uint32_t run = (tiles + 7) / 8;
       step = gridDim.x / 8;
@@ -289,11 +292,13 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
       tile = (blockIdx.x & 7) * (gridDim.x / 8) + blockIdx.x / 8;
     }
     if (tile >= end) return;
-    // the first lane that ends beyond this tile's row tile holds its expert
-    const int at = __builtin_ctzll(wave_ballot(upto > static_cast<int64_t>(tile / nt)));
-    before = uniform(__shfl(upto - mine, at));
-    walk = __builtin_amdgcn_readfirstlane(at * per);
-    te = row_tiles_of_one(walk);
+    if (g.expert_rows != nullptr) {
+      // the first lane that ends beyond this tile's row tile holds its expert
+      const int at = __builtin_ctzll(wave_ballot(upto > tile / nt));
+      before = __builtin_amdgcn_readlane(upto - mine, at);
+      walk = at * per;
+      te = row_tiles_of_one(walk);
+    }
   }
 
   // ---- the tile whose stages are being copied ----
@@ -317,12 +322,12 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
       place(q - rank * each);
     } else {
       const uint32_t q = tile / nt;
-      while (q >= static_cast<uint64_t>(before + te)) {  // ends at the expert of tile q
+      while (q >= before + te) {  // ends at the expert of tile q
         before += te;
         te = row_tiles_of_one(++walk);
       }
       at.e = walk;
-      const uint32_t local = tile - static_cast<uint32_t>(before) * nt;
+      const uint32_t local = tile - before * nt;
       place(local);
     }
     span_of_one(g.expert_rows, at.e, g.capacity, g.num_rows, at.first, at.count);
@@ -528,7 +533,8 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
       for (int j = 0; j < FM; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-    const auto stage = [&](int st, auto pc) {
+    // A stage; without products (`idle`) past the last one.
+    const auto stage = [&](int st, auto pc, auto idle) {
       constexpr int P = decltype(pc)::value;
       const uint8_t *xb = x_buf(pc), *rb = r_buf(pc);
       constexpr std::integral_constant<int, P + 1> after{};
@@ -544,7 +550,7 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
       const int sx = st + XS - 1 >= c_all ? st + XS - 1 - c_all : st + XS - 1;  // the stages to copy
       const int sr = st + RS >= c_all ? st + RS - c_all : st + RS;
       const bool no_x = last && st + XS - 1 >= c_all, no_r = last && st + RS >= c_all;
-      if (st < c_stages) {
+      if constexpr (!decltype(idle)::value) {
       __builtin_amdgcn_sched_barrier(0);
       copy_x(sx, no_x, x_buf(std::integral_constant<int, P + XS - 1>{}));
       read(1, 1, xb, rb);
@@ -570,17 +576,34 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
       multiply(1);
       interleave(std::integral_constant<int, LR>{});
       __builtin_amdgcn_sched_barrier(0);
-      } else {  // (its wait for all copies, once a tile, spares the compiler's own in the stages above)
+      } else {
         copy_x(sx, no_x, x_buf(std::integral_constant<int, P + XS - 1>{}));
         wait_copies<kAhead>();
         copy_r(sr, no_r, r_buf(pc));
-        read(0, 0, x_buf(after), r_buf(after));
-        __builtin_amdgcn_s_waitcnt(7 << 4 | 15 << 8);  // vmcnt(0)
+        if constexpr (P + 1 == kRing) read(0, 0, x_buf(after), r_buf(after));
       }
       asm volatile("" ::: "memory");  // the copies' order stays: the wait above counts on it
     };
-    for (int first = 0; first < c_all; first += kRing)
-      static_for<0, kRing>([&](auto pc) { stage(first + decltype(pc)::value, pc); });
+    // Rounds of the buffers, and a last one that is not all products (written out a
+    // second time, and with a wait for all copies at its end, so that no path leads
+    // from an idle stage's copies to products: the compiler would wait for them
+    // there, on every path).
+    const int whole = c_stages / kRing * kRing;
+    for (int first = 0; first < whole; first += kRing)
+      static_for<0, kRing>([&](auto pc) { stage(first + decltype(pc)::value, pc, std::false_type{}); });
+    if (whole < c_all) {
+      static_while<0, kRing - 1>([&](auto pc) {
+        constexpr int P = decltype(pc)::value;
+        if (whole + P >= c_stages) return false;
+        stage(whole + P, pc, std::false_type{});
+        return true;
+      });
+      static_for<0, kRing>([&](auto pc) {
+        constexpr int P = decltype(pc)::value;
+        if (whole + P >= c_stages) stage(whole + P, pc, std::true_type{});
+      });
+      __builtin_amdgcn_s_waitcnt(7 << 4 | 15 << 8);  // vmcnt(0)
+    }
 
     // ---- the result ----
     const size_t row0 = KIND == kWeights ? static_cast<size_t>(c.e) * g.M + c.m0 : static_cast<size_t>(c.first) + c.m0;
