@@ -10,7 +10,10 @@ namespace {
 // rows of a and 16 of w (the gates and ups of 8 channels, or 16 channels); its
 // eight waves split the summed channels, read their share straight into
 // registers, eight loads of 16 rows by 64 bytes ahead, and add their sums in LDS
-// in a fixed order.
+// in a fixed order.  16 rows of 7168 to 4096, gated: 16.5 us (3.6 TB/s, bounded by
+// the latency of few loads a wave), against 32 in 64 x 64 tiles, which leave half of
+// the CUs idle; 7 rows of 2048 to 7168: 9.4.  Where tiles fill the chip they are
+// faster (1 token of 8 of 256 experts: 73 against 88 us; 128 tokens 2090 against 2900).
 constexpr int kFewWaves = 8;
 
 template <bool GATED>
@@ -113,6 +116,27 @@ __global__ __launch_bounds__(kFewWaves* kWave, 4) void linear_few(const LinearAr
   }
 }
 
+// The tile, by the mean rows of an expert, and smaller where larger ones would
+// leave CUs without any.  Measured in microseconds, * as the rule picks, "once":
+// weights read non-temporally; with E 256, H 7168, N 4096 gated, 8 experts a token,
+//   tokens (mean rows)  128 (4)  512 (16)  2048 (64)  3000 (94)  4096 (128)  32768 (1024)
+//   64 x 128 once         *2088     *2234       3614
+//   64 x 128               2350      2403       3601       3789        4380
+//   128 x 256 once         2106      2256      *2397      *2571         4308
+//   128 x 256              2450      2512       2606       2656        3655        15890
+//   192 x 256              2414      2469       2671       2749       *3016        15510
+//   256 x 256              2531      2652       2880       2969        3216       *13230
+// and for one matrix of the same sizes (its rows), where few tiles are idle CUs:
+//   rows                  16   128   256   512  1024  2048
+//   few rows           *16.9   109   214   425   847  1688
+//   64 x 64             31.5  *32.4 *33.5  44.5  83.4   163
+//   64 x 128            35.5  36.2  37.5 *43.9  82.2   160
+//   128 x 128           41.4  43.4  43.5  47.4 *58.7   113
+//   128 x 256           65.4  69.2  69.5  70.2  74.5  *103
+//   256 x 256            112   113   117   117   119   137
+// With many rows on one matrix L2 serves the weights, two stages of them do, and
+// more stages cost more idle ones at a tile's end (16384 rows of 2048 to 7168: two
+// 371, three 391; 1024 rows an expert as above: 13880 and 13090).
 template <bool GATED>
 hipError_t launch(const LinearArgs& g, hipStream_t stream) {
   constexpr Kind F = kForward;

@@ -7,6 +7,20 @@
 namespace ep {
 namespace {
 
+// The tile, as for the layer itself; microseconds, * as the rule picks, with E 256,
+// N 4096 to H 7168, 8 experts a token (p: N 7168 to H 2048 through the activation):
+//   tokens (mean rows)  512 (16)  1024 (32)  2048 (64)  3000 (94)  4096 (128) p  4096 popular
+//   64 x 128                2711       2854       3385       4226          2583          5351
+//   128 x 128               2655       2827       3148       3364          2590          4505
+//   128 x 256               2635       2771       2934       3038          2492          4052
+//   192 x 256              *2518      *2616      *2761      *2947         *1593         *3846
+//   256 x 256               2730       2844       3027       3145          1760          4023
+// and for one matrix:
+//   rows                 128   512  1024  2048  4096
+//   64 x 128           *25.7  52.0  93.8   177   330
+//   128 x 128           30.7 *35.1  66.4   128   240
+//   128 x 256           45.8  48.2 *58.1   115   224
+//   256 x 256           74.0  76.6  79.3  *102  *202
 template <bool GATED>
 hipError_t launch(const LinearArgs& g, hipStream_t stream) {
   const LinearShape s = linear_shape(g);

@@ -6,6 +6,14 @@
 namespace ep {
 namespace {
 
+// The tile, by the mean rows of an expert and by how many tiles there are (in
+// microseconds, * as the rule picks, bf16):
+//   experts x rows, N x H   256 x 128, 1024 x 2048   64 x 512, same   32 x 1024, 4096 x 7168   1 x 8192, 2048 x 2048
+//   128 x 128                                  530              272                     2424                     *75
+//   128 x 256                                 *426              206                     2010                     113
+//   256 x 256                                  485             *210                    *1841                     206
+// Few tiles of a long sum are not split: 512 x 512 over 32768 rows keeps 16
+// workgroups busy for 205 us.
 template <typename T>
 hipError_t launch(const LinearArgs& g, hipStream_t stream) {
   const int64_t cus = max(device_cu_count(), 1);

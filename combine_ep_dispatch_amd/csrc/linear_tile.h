@@ -17,7 +17,21 @@
 // it lies as 64 rows of BN (BM) elements and is read through gfx950's
 // transposing LDS load: sixteen lanes read four rows of sixteen elements, and
 // each gets the four of its column.  Both kinds hold their 16-byte pieces
-// permuted, so that lanes served together meet different banks.
+// permuted, so that lanes served together meet different banks (counted: 1 to 6
+// conflicts in 100 LDS cycles).
+//
+// Sums are binary32: the bf16 MFMA keeps them (products exact, a term 2^-23 below
+// the sum counts in full, subnormals kept), and every result is rounded once.
+//
+// What bounds it: 8192^3 takes 803 to 840 us in all three kinds (1310 to 1370
+// TFLOP/s; the matrix unit is busy 84% of the time, at 1.4 GHz: the card's power
+// limit).  With 256 experts of 7168 to 4096 (gated) the weights stream in at 7.1
+// TB/s where an expert has few rows; at 128 rows an expert both bounds meet (5.3
+// TB/s, 650 TFLOP/s, 1.3 GHz); at 1024 rows 1180 TFLOP/s.  Measured without gain:
+// half a tile's products where an expert's last rows fit that (3% at 128 rows, but
+// tiles that drift apart lose their shared lines in L2: 14.6 against 13.0 ms at 1024
+// rows), four waves of 128 x 128, all of a stage's fragments read at once,
+// non-temporal stores of the result.
 #pragma once
 
 #include "ep_internal.h"
@@ -26,9 +40,7 @@
 namespace ep {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 enum Kind { kForward, kRows, kWeights };
@@ -204,8 +216,8 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
   constexpr bool kRuns = KIND != kWeights && BM <= 128;
   // kWeights: every expert has the same tiles, but sums of its own length.  The
   // experts go by falling length, and every other turn is dealt backwards, so that
-  // no workgroup is left with a long sum at the end (32 experts, popular ones: 960
-  // against 1200 us).  order: this lane's experts in that order, the 64 i-th on,
+  // no workgroup is left with a long sum at the end (32 experts, popular ones: 1309
+  // against 1349 us).  order: this lane's experts in that order, the 64 i-th on,
   // two in a register.
   uint32_t order[KIND == kWeights ? kMaxExperts / kWave / 2 : 1];
   if constexpr (KIND == kWeights) {
@@ -306,7 +318,8 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
     int e, first, count, m0, n0;  // expert, its rows, the tile's first row and channel
   } at;
   // An expert's tiles go in bands of eight row tiles, channel by channel, so that
-  // the 32 workgroups of an XCD read 8 + 4 operands' tiles at a time.
+  // the 32 workgroups of an XCD read 8 + 4 operands' tiles at a time, not 32 + 1
+  // (8192^3: 870 against 1009 us).
   const auto place = [&](uint32_t local) {
     const uint32_t band = local / (8 * nt), rest = local - band * 8 * nt, width = min(te - band * 8, 8u);
     at.m0 = static_cast<int>(band * 8 + rest % width) * BM;
@@ -431,7 +444,7 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
   // Where this lane reads: along, of fragment 0 by 16-element step; across, of
   // step 0 by fragment.  (Opaque to the compiler: it would split them into sums of
   // many terms, at the end of which it loses which buffer an address is in and waits
-  // for every copy.)
+  // for every copy: across, 8192^3 took 929 us, and 840 so.)
   uint32_t xa[kXAlong ? 4 : FN], ra[kRAlong ? 4 : FM];
   const auto lane_along = [&](int row, int ks) {
     uint32_t v = (row + col) * 128 + ((ks * 2 + half) ^ along_swizzle(col)) * 16;
@@ -482,7 +495,8 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(xv[set][i], rv[set][j], acc[i][j], 0, 0, 0);
   };
   // One product, then its share of the next fragments' reads and of the copies,
-  // and so on: copies issued together would keep the wave from its products.
+  // and so on: copies issued together would keep the wave from its products (8192^3:
+  // 1050 to 1060 us, and 883 to 1009 spread out).
   constexpr int kReads = FN * (kXAlong ? 1 : 2) + FM * (kRAlong ? 1 : 2), kMul = FN * FM;
   const auto interleave = [&](auto copies) {
     constexpr int kCopies = decltype(copies)::value;
@@ -517,7 +531,8 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
     const int c_all = max((c_stages + kRing - 1) / kRing, 1) * kRing;
     const bool live = wm * 32 < c_rows;  // else this wave's rows are all past the end
     // The tiles of the first channels sum R's columns as well, from the stages in
-    // LDS: each lane eight columns of every kAtOnce-th row.
+    // LDS: each lane eight columns of every kAtOnce-th row.  (32768 rows of 7168: 866 us
+    // in all, and 961 with a kernel that reads R again.)
     constexpr int kPieces = BM / 8, kAtOnce = NW * kWave / kPieces;
     const bool c_sums = KIND == kWeights && g.sums != nullptr && c.n0 == 0;
     f32x8 columns = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -551,31 +566,31 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
       const int sr = st + RS >= c_all ? st + RS - c_all : st + RS;
       const bool no_x = last && st + XS - 1 >= c_all, no_r = last && st + RS >= c_all;
       if constexpr (!decltype(idle)::value) {
-      __builtin_amdgcn_sched_barrier(0);
-      copy_x(sx, no_x, x_buf(std::integral_constant<int, P + XS - 1>{}));
-      read(1, 1, xb, rb);
-      multiply(0);
-      interleave(std::integral_constant<int, LX>{});
-      __builtin_amdgcn_sched_barrier(0);
-      read(0, 2, xb, rb);
-      multiply(1);
-      interleave(std::integral_constant<int, 0>{});
-      __builtin_amdgcn_sched_barrier(0);
-      read(1, 3, xb, rb);
-      multiply(0);
-      interleave(std::integral_constant<int, 0>{});
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (KIND == kWeights) {
-        if (c_sums) add_columns(rb);
-      }
-      // the next stage has arrived, and this one's buffers are read
-      wait_copies<kAhead>();
-      __builtin_amdgcn_sched_barrier(0);
-      copy_r(sr, no_r, r_buf(pc));
-      read(0, 0, x_buf(after), r_buf(after));
-      multiply(1);
-      interleave(std::integral_constant<int, LR>{});
-      __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);
+        copy_x(sx, no_x, x_buf(std::integral_constant<int, P + XS - 1>{}));
+        read(1, 1, xb, rb);
+        multiply(0);
+        interleave(std::integral_constant<int, LX>{});
+        __builtin_amdgcn_sched_barrier(0);
+        read(0, 2, xb, rb);
+        multiply(1);
+        interleave(std::integral_constant<int, 0>{});
+        __builtin_amdgcn_sched_barrier(0);
+        read(1, 3, xb, rb);
+        multiply(0);
+        interleave(std::integral_constant<int, 0>{});
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (KIND == kWeights) {
+          if (c_sums) add_columns(rb);
+        }
+        // the next stage has arrived, and this one's buffers are read
+        wait_copies<kAhead>();
+        __builtin_amdgcn_sched_barrier(0);
+        copy_r(sr, no_r, r_buf(pc));
+        read(0, 0, x_buf(after), r_buf(after));
+        multiply(1);
+        interleave(std::integral_constant<int, LR>{});
+        __builtin_amdgcn_sched_barrier(0);
       } else {
         copy_x(sx, no_x, x_buf(std::integral_constant<int, P + XS - 1>{}));
         wait_copies<kAhead>();
@@ -629,7 +644,8 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
     // X goes, behind the barrier below), so that four lanes hold 32 channels of a
     // row and store 64 bytes (from the accumulators' layout it would be 8).  What a
     // fragment needs from memory is read before the one before it is stored: a
-    // wait for loads is one for the stores ahead of them.  Rows and channels past the
+    // wait for loads is one for the stores ahead of them (4096 rows of 2048 to 7168 with
+    // a residual: 121 against 131 us).  Rows and channels past the
     // end are past the end of the buffer resources, where nothing is read or written.
     uint8_t* const yb = x_buf(std::integral_constant<int, XS - 1>{}) + wave * 4096;
     const auto y_place = [](uint32_t row, uint32_t piece) { return row * 128 + ((piece ^ (row & 7)) * 16); };
