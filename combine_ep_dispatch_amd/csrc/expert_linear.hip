@@ -11,7 +11,7 @@ namespace {
 // eight waves split the summed channels, read their share straight into
 // registers, eight loads of 16 rows by 64 bytes ahead, and add their sums in LDS
 // in a fixed order.  16 rows of 7168 to 4096, gated: 16.5 us (3.6 TB/s, bounded by
-// the latency of few loads a wave), against 32 in 64 x 64 tiles, which leave half of
+// the latency of few loads a wave), against 23 in 64 x 64 tiles, which leave half of
 // the CUs idle; 7 rows of 2048 to 7168: 9.4.  Where tiles fill the chip they are
 // faster (1 token of 8 of 256 experts: 73 against 88 us; 128 tokens 2090 against 2900).
 constexpr int kFewWaves = 8;
@@ -127,13 +127,17 @@ __global__ __launch_bounds__(kFewWaves* kWave, 4) void linear_few(const LinearAr
 //   192 x 256              2414      2469       2671       2749       *3016        15510
 //   256 x 256              2531      2652       2880       2969        3216       *13230
 // and for one matrix of the same sizes (its rows), where few tiles are idle CUs:
-//   rows                  16   128   256   512  1024  2048
-//   few rows           *16.9   109   214   425   847  1688
-//   64 x 64             31.5  *32.4 *33.5  44.5  83.4   163
-//   64 x 128            35.5  36.2  37.5 *43.9  82.2   160
-//   128 x 128           41.4  43.4  43.5  47.4 *58.7   113
-//   128 x 256           65.4  69.2  69.5  70.2  74.5  *103
-//   256 x 256            112   113   117   117   119   137
+//   rows                  16    64   128   256   384   512   768  1024  2048
+//   few rows           *16.2          109   214         425         847  1688
+//   64 x 64, 2 groups   23.2 *24.7 *24.9 *26.0  46.6  48.4  70.4
+//   64 x 64             31.3  31.6  31.8  32.6  41.2  42.8  72.9  83.4   163
+//   64 x 128, 2 groups  31.4  33.9  33.8  34.2 *35.2 *39.4  70.1
+//   64 x 128            35.5        36.2  37.5  41.6  41.4 *75.2  82.2   160
+//   128 x 128           41.4        43.4  43.5        47.4       *58.7   113
+//   128 x 256           65.4        69.2  69.5        70.2        74.5  *103
+//   256 x 256            112         113   117         117         119   137
+// (2048 to 7168, 128 rows: 11.1 with two groups, 12.5 with one; 256 rows: 15.4 and 17.1.
+// Three and four groups, of fewer stages each: 25.7 and 33.3 us at 128 rows.)
 // With many rows on one matrix L2 serves the weights, two stages of them do, and
 // more stages cost more idle ones at a tile's end (16384 rows of 2048 to 7168: two
 // 371, three 391; 1024 rows an expert as above: 13880 and 13090).
@@ -152,13 +156,14 @@ hipError_t launch(const LinearArgs& g, hipStream_t stream) {
     return launch_tiles<F, GATED, __bf16, 128, 256, 2, 4, 3, 3, 1>(g, stream);
   }
   if (s.avg > 32 && fill(128, 128)) return launch_tiles<F, GATED, __bf16, 128, 128, 2, 2, 4, 4, 1>(g, stream);
-  if (fill(64, 128)) {
-    if (s.avg <= 64) return launch_tiles<F, GATED, __bf16, 64, 128, 2, 2, 6, 6, 1, true>(g, stream);
-    return launch_tiles<F, GATED, __bf16, 64, 128, 2, 2, 6, 6, 1>(g, stream);
-  }
+  if (s.avg <= 64 && fill(64, 128)) return launch_tiles<F, GATED, __bf16, 64, 128, 2, 2, 6, 6, 1, true>(g, stream);
   if (s.avg <= 16 && static_cast<int64_t>(g.O) * g.C < (GATED ? int64_t(1) << 29 : int64_t(1) << 30))
     return launch_linear(linear_few<GATED>, kFewWaves * kWave, 2, g, stream);
-  return launch_tiles<F, GATED, __bf16, 64, 64, 2, 1, 4, 4, 2>(g, stream);
+  if (s.tiles(64, g.O, GATED ? 32 : 64) <= s.cus)
+    return launch_tiles<F, GATED, __bf16, 64, 64, 2, 1, 4, 4, 1, false, 2>(g, stream);
+  if (s.tiles(64, g.O, GATED ? 64 : 128) <= s.cus)
+    return launch_tiles<F, GATED, __bf16, 64, 128, 2, 2, 3, 3, 1, false, 2>(g, stream);
+  return launch_tiles<F, GATED, __bf16, 64, 128, 2, 2, 6, 6, 1>(g, stream);
 }
 
 }  // namespace

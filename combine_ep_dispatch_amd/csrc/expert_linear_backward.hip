@@ -17,10 +17,13 @@ namespace {
 //   256 x 256               2730       2844       3027       3145          1760          4023
 // and for one matrix:
 //   rows                 128   512  1024  2048  4096
-//   64 x 128           *25.7  52.0  93.8   177   330
+//   64 x 128, 2 groups *24.0  45.3
+//   64 x 128            25.3  47.4  93.8   177   330
 //   128 x 128           30.7 *35.1  66.4   128   240
 //   128 x 256           45.8  48.2 *58.1   115   224
 //   256 x 256           74.0  76.6  79.3  *102  *202
+// (7168 to 2048, through the activation, 64 x 128: 128 rows 35.0 in two groups and 40.8
+// in one, 1024 rows 41.9 and 46.6.)
 template <bool GATED>
 hipError_t launch(const LinearArgs& g, hipStream_t stream) {
   const LinearShape s = linear_shape(g);
@@ -31,6 +34,8 @@ hipError_t launch(const LinearArgs& g, hipStream_t stream) {
   if (s.fill(192, g.O, 256)) return launch_tiles<kRows, GATED, __bf16, 192, 256, 2, 4, 3, 2, 1>(g, stream);
   if (s.fill(128, g.O, 256)) return launch_tiles<kRows, GATED, __bf16, 128, 256, 2, 4, 3, 3, 1>(g, stream);
   if (s.fill(128, g.O, 128)) return launch_tiles<kRows, GATED, __bf16, 128, 128, 2, 2, 4, 4, 1>(g, stream);
+  if (s.tiles(64, g.O, 128) <= s.cus)
+    return launch_tiles<kRows, GATED, __bf16, 64, 128, 2, 2, 3, 3, 1, false, 2>(g, stream);
   return launch_tiles<kRows, GATED, __bf16, 64, 128, 2, 2, 6, 6, 1>(g, stream);
 }
 

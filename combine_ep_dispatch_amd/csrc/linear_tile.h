@@ -147,9 +147,11 @@ __device__ __forceinline__ void copy_piece(Rsrc src, uint8_t* dst, uint32_t lane
 constexpr uint32_t kNone = 0x80000000u;
 
 // WM x WN: the tile's waves; XS, RS: stages of X and of R kept; PER: workgroups
-// of a CU; ONCE: X is read non-temporally.
-template <Kind KIND, bool GATED, typename T, int BM, int BN, int WM, int WN, int XS, int RS, int PER, bool ONCE>
-__global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear_tiled(const LinearArgs g) {
+// of a CU; ONCE: X is read non-temporally; G: groups of WM x WN waves, each with
+// buffers of its own, that take a part of the summed channels each (where there are
+// fewer tiles than CUs: a stage's waits then serve G of them).
+template <Kind KIND, bool GATED, typename T, int BM, int BN, int WM, int WN, int XS, int RS, int PER, bool ONCE, int G>
+__global__ __launch_bounds__(G* WM* WN* kWave, (G * WM * WN * PER + 3) / 4) void linear_tiled(const LinearArgs g) {
   constexpr int NW = WM * WN;
   constexpr bool kPair = KIND == kForward && GATED;  // X holds gate and up rows of the same BO channels
   constexpr bool kXAlong = KIND == kForward, kRAlong = KIND != kWeights;
@@ -164,7 +166,8 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
   static_assert(XS == RS || XS == RS + 1, "the order of the copies");
   constexpr int kRing = XS == RS ? XS : XS * RS;  // stages after which the buffers repeat
   static_assert(XS <= 6 && RS <= 6, "buffers");
-#define EP_BUFFER(name, i, n, rows) __shared__ __align__(16) uint8_t name##i[(n) > i ? (rows) * 128 : 16]
+  static_assert(G == 1 || KIND != kWeights, "the column sums are one group's");
+#define EP_BUFFER(name, i, n, rows) __shared__ __align__(16) uint8_t name##i[(n) > i ? G * (rows) * 128 : 16]
   EP_BUFFER(x, 0, XS, BN);  // (arrays of their own: the compiler tells copies into one from reads of another)
   EP_BUFFER(x, 1, XS, BN);
   EP_BUFFER(x, 2, XS, BN);
@@ -178,26 +181,29 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
   EP_BUFFER(r, 4, RS, BM);
   EP_BUFFER(r, 5, RS, BM);
 #undef EP_BUFFER
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave) % NW;  // of its group
+  const int group = G == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid / kWave) / NW;
   const auto x_buf = [&](auto qc) -> uint8_t* {
     constexpr int q = decltype(qc)::value % XS;
-    if constexpr (q == 0) return x0;
-    else if constexpr (q == 1) return x1;
-    else if constexpr (q == 2) return x2;
-    else if constexpr (q == 3) return x3;
-    else if constexpr (q == 4) return x4;
-    else return x5;
+    const int mine = group * BN * 128;
+    if constexpr (q == 0) return x0 + mine;
+    else if constexpr (q == 1) return x1 + mine;
+    else if constexpr (q == 2) return x2 + mine;
+    else if constexpr (q == 3) return x3 + mine;
+    else if constexpr (q == 4) return x4 + mine;
+    else return x5 + mine;
   };
   const auto r_buf = [&](auto qc) -> uint8_t* {
     constexpr int q = decltype(qc)::value % RS;
-    if constexpr (q == 0) return r0;
-    else if constexpr (q == 1) return r1;
-    else if constexpr (q == 2) return r2;
-    else if constexpr (q == 3) return r3;
-    else if constexpr (q == 4) return r4;
-    else return r5;
+    const int mine = group * BM * 128;
+    if constexpr (q == 0) return r0 + mine;
+    else if constexpr (q == 1) return r1 + mine;
+    else if constexpr (q == 2) return r2 + mine;
+    else if constexpr (q == 3) return r3 + mine;
+    else if constexpr (q == 4) return r4 + mine;
+    else return r5 + mine;
   };
-  const int tid = threadIdx.x, lane = tid & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int half = lane >> 5, col = lane & 31;
   const int wm = wave % WM, wn = wave / WM;
   const int O = g.O;
@@ -345,7 +351,9 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
     }
     span_of_one(g.expert_rows, at.e, g.capacity, g.num_rows, at.first, at.count);
   };
-  const auto stages_of = [&](const Place& t) { return ((KIND == kWeights ? t.count : g.C) + 63) / 64; };
+  const auto stages_of = [&](const Place& t) { return ((KIND == kWeights ? t.count : g.C) + 63) / 64; };  // of all groups
+  const auto share = [&](int stages) { return G == 1 ? stages : (stages + G - 1) / G; };
+  const int ahead = G == 1 ? 0 : group * share((g.C + 63) / 64);  // stages of the groups before
   const auto rows_in = [&](const Place& t) { return min((KIND == kWeights ? g.M : t.count) - t.m0, BM); };
 
   // An operand's copies.  Along: piece (lane & 7) of row lane / 8 of eight, and
@@ -408,7 +416,8 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
     }
   };
   const auto copy_x = [&](int s, bool none, uint8_t* buf) {
-    none = none || s >= x_stages;
+    none = none || s >= share(x_stages) || (G > 1 && s + ahead >= x_stages);
+    s += ahead;
     if constexpr (kXAlong) {
       const uint32_t gone = none || (s == x_stages - 1 && along_cut) ? kNone : 0;
 #pragma unroll
@@ -422,7 +431,8 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
     }
   };
   const auto copy_r = [&](int s, bool none, uint8_t* buf) {
-    none = none || s >= r_stages;
+    none = none || s >= share(r_stages) || (G > 1 && s + ahead >= r_stages);
+    s += ahead;
     if constexpr (kRAlong) {
       const uint32_t gone = none || (s == r_stages - 1 && along_cut) ? kNone : 0;
 #pragma unroll
@@ -523,10 +533,10 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
     asm volatile("" ::: "memory");
   });
   wait_copies<(XS - 2) * LX + (RS - 1) * LR>();
-  read(0, 0, x0, r0);
+  read(0, 0, x_buf(std::integral_constant<int, 0>{}), r_buf(std::integral_constant<int, 0>{}));
   for (;;) {
     const Place c = at;  // the tile being multiplied
-    const int c_rows = rows_in(c), c_stages = stages_of(c);
+    const int c_rows = rows_in(c), c_stages = share(stages_of(c));
     // its stages, and none or more without products, so that each tile starts with the same buffers
     const int c_all = max((c_stages + kRing - 1) / kRing, 1) * kRing;
     const bool live = wm * 32 < c_rows;  // else this wave's rows are all past the end
@@ -778,7 +788,30 @@ __global__ __launch_bounds__(WM* WN* kWave, (WM * WN * PER + 3) / 4) void linear
         }
       }
     };
-    if (live && !(adds && c_stages == 0)) {
+    if constexpr (G > 1) {  // the groups' sums, in their order, a fragment at a time
+      static_for<0, FN * FM>([&](auto fc) {
+        constexpr int i = decltype(fc)::value % FN, j = decltype(fc)::value / FN;
+        if (group != 0) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4*>(yb + q * 1024 + lane * 16) =
+                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        }
+        wait_reads();
+        if (group == 0) {
+#pragma unroll
+          for (int o = 1; o < G; ++o)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f32x4 v = *reinterpret_cast<const f32x4*>(yb + o * BN * 128 + q * 1024 + lane * 16);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) acc[i][j][4 * q + x] += v[x];
+            }
+        }
+        wait_reads();
+      });
+    }
+    if (live && group == 0 && !(adds && c_stages == 0)) {
       fetch(0);
       static_while<0, kFragments>([&](auto fc) {
         constexpr int f = decltype(fc)::value;
@@ -800,9 +833,9 @@ hipError_t launch_linear(Kernel kernel, int threads, int per_cu, const LinearArg
   hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), 0, stream, g);
   return hipGetLastError();
 }
-template <Kind KIND, bool GATED, typename T, int BM, int BN, int WM, int WN, int XS, int RS, int PER, bool ONCE = false>
+template <Kind KIND, bool GATED, typename T, int BM, int BN, int WM, int WN, int XS, int RS, int PER, bool ONCE = false, int G = 1>
 hipError_t launch_tiles(const LinearArgs& g, hipStream_t stream) {
-  return launch_linear(linear_tiled<KIND, GATED, T, BM, BN, WM, WN, XS, RS, PER, ONCE>, WM * WN * kWave, PER, g, stream);
+  return launch_linear(linear_tiled<KIND, GATED, T, BM, BN, WM, WN, XS, RS, PER, ONCE, G>, G * WM * WN * kWave, PER, g, stream);
 }
 
 // What the choice of a tile goes by.  The rows of each expert are on the device;
@@ -812,11 +845,10 @@ struct LinearShape {
   int64_t rows, hit;  // and experts that have any, at most
   int64_t avg;        // rows of an expert
   int64_t cus;
-  // Tiles of bm rows and bo of o channels fill the chip, or nearly.
-  bool fill(int bm, int o, int bo) const {
-    const int64_t row_tiles = max(hit, (rows + bm - 1) / bm);
-    return row_tiles * ((o + bo - 1) / bo) * 8 >= 7 * cus;
+  int64_t tiles(int bm, int o, int bo) const {  // of bm rows and bo of o channels
+    return max(hit, (rows + bm - 1) / bm) * ((o + bo - 1) / bo);
   }
+  bool fill(int bm, int o, int bo) const { return tiles(bm, o, bo) * 8 >= 7 * cus; }  // the chip, or nearly
 };
 inline LinearShape linear_shape(const LinearArgs& g) {
   const int64_t each = g.capacity > 0 ? min(g.capacity, 64) : g.num_rows / g.E;

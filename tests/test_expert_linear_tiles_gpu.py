@@ -21,7 +21,8 @@ def ragged(experts, rows, seed):
 # rows (dense, or experts and mean rows), channels of the result
 TILES = {"256x256 dense": (4100, 4400), "256x256": ((8, 560), 4400), "192x256": ((70, 135), 1304), "128x256": ((70, 55), 1304),
          "128x256 dense": (1100, 8000), "128x128": (600, 6400), "64x128": ((70, 7), 704), "64x128 dense": (500, 3800),
-         "64x64": (40, 1000), "few rows": (13, 1000), "few rows of few experts": ((5, 3), 200)}
+         "64x128 of 352": (700, 4000), "64x128 in groups, more than CUs": ((20, 75), 1240),
+         "64x64": (40, 1000), "64x64, more than CUs": ((20, 75), 600), "few rows": (13, 1000), "few rows of few experts": ((5, 3), 200)}
 
 
 def rows_of(rows):
