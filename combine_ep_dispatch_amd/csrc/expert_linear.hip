@@ -136,8 +136,15 @@ __global__ __launch_bounds__(kFewWaves* kWave, 4) void linear_few(const LinearAr
 //   128 x 128           41.4        43.4  43.5        47.4       *58.7   113
 //   128 x 256           65.4        69.2  69.5        70.2        74.5  *103
 //   256 x 256            112         113   117         117         119   137
-// (2048 to 7168, 128 rows: 11.1 with two groups, 12.5 with one; 256 rows: 15.4 and 17.1.
-// Three and four groups, of fewer stages each: 25.7 and 33.3 us at 128 rows.)
+// Three and four groups, of fewer stages each, take 25.7 and 33.3 us at 128 rows.
+// Two groups need a long sum (the second one's way to the first costs 2 us):
+//   summed channels                256   512  1024  2048  4096
+//   128 rows, N 1024:
+//     64 x 64, 2 groups            6.2   6.1  *7.3  *9.9 *15.5
+//     64 x 64                     *4.6  *5.6   7.6  11.5  19.8
+//   384 rows, N 4096 gated:
+//     64 x 128, 2 groups           7.2   8.4  10.5  14.9 *23.0
+//     64 x 64                     *6.1  *7.2 *10.0 *14.8  24.5
 // With many rows on one matrix L2 serves the weights, two stages of them do, and
 // more stages cost more idle ones at a tile's end (16384 rows of 2048 to 7168: two
 // 371, three 391; 1024 rows an expert as above: 13880 and 13090).
@@ -159,10 +166,12 @@ hipError_t launch(const LinearArgs& g, hipStream_t stream) {
   if (s.avg <= 64 && fill(64, 128)) return launch_tiles<F, GATED, __bf16, 64, 128, 2, 2, 6, 6, 1, true>(g, stream);
   if (s.avg <= 16 && static_cast<int64_t>(g.O) * g.C < (GATED ? int64_t(1) << 29 : int64_t(1) << 30))
     return launch_linear(linear_few<GATED>, kFewWaves * kWave, 2, g, stream);
-  if (s.tiles(64, g.O, GATED ? 32 : 64) <= s.cus)
+  if (g.C > 768 && s.tiles(64, g.O, GATED ? 32 : 64) <= s.cus)
     return launch_tiles<F, GATED, __bf16, 64, 64, 2, 1, 4, 4, 1, false, 2>(g, stream);
-  if (s.tiles(64, g.O, GATED ? 64 : 128) <= s.cus)
-    return launch_tiles<F, GATED, __bf16, 64, 128, 2, 2, 3, 3, 1, false, 2>(g, stream);
+  if (s.tiles(64, g.O, GATED ? 64 : 128) <= s.cus) {
+    if (g.C > 2048) return launch_tiles<F, GATED, __bf16, 64, 128, 2, 2, 3, 3, 1, false, 2>(g, stream);
+    return launch_tiles<F, GATED, __bf16, 64, 64, 2, 1, 4, 4, 2>(g, stream);
+  }
   return launch_tiles<F, GATED, __bf16, 64, 128, 2, 2, 6, 6, 1>(g, stream);
 }
 

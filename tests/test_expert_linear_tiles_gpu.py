@@ -38,6 +38,13 @@ def test_linear_tiles(gpu, tile, C):
     forward(gpu, r, C, 16 * (O // 16), gated=True, save=C == 448, bias=C == 56, whole=C != 1000)
 
 
+@pytest.mark.parametrize("rows,O", [(500, 3800), ((20, 75), 1240)], ids=["dense", "more than CUs"])
+def test_linear_long_sums_in_groups(gpu, rows, O):
+    r = rows_of(rows)
+    forward(gpu, r, 2056, O, bias=True, residual=True)
+    forward(gpu, r, 2056, O // 16 * 16, gated=True, save=True, whole=False)
+
+
 @pytest.mark.parametrize("C", [56, 448, 1000])
 @pytest.mark.parametrize("tile", TILES)
 def test_backward_tiles(gpu, tile, C):
