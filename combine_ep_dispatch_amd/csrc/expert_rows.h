@@ -22,6 +22,10 @@ EP_ROWS_FN void span_rows(int32_t begin, int32_t end, int32_t num_rows, int32_t&
   count = last - first;
 }
 
+// Stages of 64 elements of a sum of n (as many as 2^31 - 1 rows: n + 63 need not
+// fit an int).
+EP_ROWS_FN int32_t stages_of_sum(int32_t n) { return static_cast<int32_t>((static_cast<uint32_t>(n) + 63) / 64); }
+
 // A number of row tiles.  Wild offsets may span the whole buffer for every
 // other expert: 512 times 2^27 rows in tiles of 16 are 2^32.
 typedef int64_t RowTiles;

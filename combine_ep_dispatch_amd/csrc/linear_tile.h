@@ -351,9 +351,9 @@ __global__ __launch_bounds__(G* WM* WN* kWave, (G * WM * WN * PER + 3) / 4) void
     }
     span_of_one(g.expert_rows, at.e, g.capacity, g.num_rows, at.first, at.count);
   };
-  const auto stages_of = [&](const Place& t) { return ((KIND == kWeights ? t.count : g.C) + 63) / 64; };  // of all groups
+  const auto stages_of = [&](const Place& t) { return stages_of_sum(KIND == kWeights ? t.count : g.C); };  // of all groups
   const auto share = [&](int stages) { return G == 1 ? stages : (stages + G - 1) / G; };
-  const int ahead = G == 1 ? 0 : group * share((g.C + 63) / 64);  // stages of the groups before
+  const int ahead = G == 1 ? 0 : group * share(stages_of_sum(g.C));  // stages of the groups before
   const auto rows_in = [&](const Place& t) { return min((KIND == kWeights ? g.M : t.count) - t.m0, BM); };
 
   // An operand's copies.  Along: piece (lane & 7) of row lane / 8 of eight, and
