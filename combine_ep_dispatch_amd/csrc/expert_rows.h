@@ -26,6 +26,17 @@ EP_ROWS_FN void span_rows(int32_t begin, int32_t end, int32_t num_rows, int32_t&
 // fit an int).
 EP_ROWS_FN int32_t stages_of_sum(int32_t n) { return static_cast<int32_t>((static_cast<uint32_t>(n) + 63) / 64); }
 
+// Tiles of a launch: its row tiles by nt tiles of channels, or none where they
+// reach 2^30.  Rows that lie apart stay far below; offsets that run back may let
+// experts share rows so often that 32 bits would not hold the sum, and then nothing
+// is computed rather than a part.  row_tiles is a sum of at most 64 addends modulo
+// 2^32, high the same sum of the addends' upper halves: below 2^14 of those the
+// sum is below 2^30 + 2^22 and has not wrapped.
+EP_ROWS_FN uint32_t tiles_or_none(uint32_t row_tiles, uint32_t high, uint32_t nt) {
+  const uint64_t tiles = static_cast<uint64_t>(row_tiles) * nt;
+  return high >= 1u << 14 || tiles >= 1u << 30 ? 0 : static_cast<uint32_t>(tiles);
+}
+
 // A number of row tiles.  Wild offsets may span the whole buffer for every
 // other expert: 512 times 2^27 rows in tiles of 16 are 2^32.
 typedef int64_t RowTiles;

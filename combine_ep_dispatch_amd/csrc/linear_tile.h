@@ -272,13 +272,12 @@ __global__ __launch_bounds__(G* WM* WN* kWave, (G * WM * WN * PER + 3) / 4) void
   int walk = 0;
   if constexpr (KIND == kWeights) {
     te = (g.M + BM - 1) / BM;
-    const uint64_t all = static_cast<uint64_t>(te) * nt * E;
-    end = static_cast<uint32_t>(min(all, static_cast<uint64_t>(0x40000000)));
+    end = te * nt * E;  // at most 2^9 * 2^9 * 2^10
     step = gridDim.x;
     tile = (blockIdx.x & 7) * (gridDim.x / 8) + blockIdx.x / 8;
     if (tile >= end) return;
   } else {
-    uint32_t mine = 0, upto = 0, total;
+    uint32_t mine = 0, upto = 0, total, high = 0;
     const int per = (E + kWave - 1) / kWave;  // experts of a lane
     if (g.expert_rows == nullptr) {
       total = te = row_tiles_of_one(0);
@@ -292,13 +291,9 @@ __global__ __launch_bounds__(G* WM* WN* kWave, (G * WM * WN * PER + 3) / 4) void
       }
       upto = wave_inclusive_scan(mine);
       total = __builtin_amdgcn_readlane(upto, kWave - 1);
-      // Rows that lie apart are below 2^26 row tiles; where offsets out of order let
-      // experts share rows so often that the sums could pass 32 bits, nothing is done.
-      const uint32_t high = __builtin_amdgcn_readlane(wave_inclusive_scan(mine >> 16), kWave - 1);
-      if (high >= 1 << 14) return;
+      high = __builtin_amdgcn_readlane(wave_inclusive_scan(mine >> 16), kWave - 1);
     }
-    // (2^30 tiles at most)
-    const uint32_t tiles = static_cast<uint32_t>(min(static_cast<uint64_t>(total) * nt, static_cast<uint64_t>(0x40000000)));
+    const uint32_t tiles = tiles_or_none(total, high, nt);
     if constexpr (kRuns) {
       const uint32_t run = (tiles + 7) / 8;
       step = gridDim.x / 8;

@@ -510,7 +510,11 @@ ep_status ep_expert_product(const void* a, const void* a_scale, int32_t a_format
  * bias         bf16 [E, N] or NULL
  * residual     bf16 of y's shape or NULL; may be y itself
  * expert_rows  as ep_expert_product's; NULL (E == 1, capacity == 0): every
- *              row is expert 0's
+ *              row is expert 0's.  Offsets that run back make rows several
+ *              experts' at once: what such a row of y, p or grad_a holds
+ *              afterwards is not defined, and where the result would have
+ *              2^30 tiles or more (with offsets in order there are fewer than
+ *              2^27) none of its rows is written
  * p            bf16 [num_rows, N] out or NULL: p rounded to BF16, what
  *              ep_expert_linear_backward needs of a gated layer
  *              (EP_ACT_SWIGLU only)
