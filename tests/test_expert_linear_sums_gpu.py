@@ -59,7 +59,7 @@ def test_large_terms_cancel_exactly(gpu, tile, C):
     check(grad_a, *want, True, "grad_a")
 
 
-WEIGHTS = [([1000, 0, 1, 450, 900], 1800, 2304), ([40] * 70, 600, 704), (2056, 304, 200), ([64, 0, 70], 136, 520), (257, 8, 16)]
+WEIGHTS = [([1000, 0, 1, 450, 900], 1800, 2304), ([40] * 70, 600, 704), (2056, 304, 200), ([64, 0, 70], 136, 520), (257, 8, 16), (32768, 264, 520)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -174,3 +174,23 @@ def test_gates_whose_sigmoid_is_below_binary32(gpu):
     y = sentinel(R, H)
     ep.ep_expert_linear(dev(a), dev(w), None, 0, ep.EP_ACT_SWIGLU, y)
     check(y, *want, False, "y")
+
+
+def test_a_long_sum_is_the_same_in_both_types(gpu):
+    """32768 rows of one matrix: the same bits on every run, BF16 the rounding
+    of the binary32 sums, and both within their bound."""
+    ep = gpu
+    R, H, N = 32768, 264, 520
+    rng = np.random.default_rng(2)
+    g, a = dev(rng.standard_normal((R, N))), dev(rng.standard_normal((R, H)))
+    print("case long sum", flush=True)
+    wide = ep.expert_linear_backward_weights(g, a, None, torch.float32, bias=True)
+    narrow = ep.expert_linear_backward_weights(g, a, None, bias=True)
+    for _ in range(3):
+        again = ep.expert_linear_backward_weights(g, a, None, torch.float32, bias=True)
+        assert all(torch.equal(x, y) for x, y in zip(wide, again))
+    assert all(torch.equal(x.bfloat16(), y) for x, y in zip(wide, narrow))
+    want = ops.expert_linear_backward_weights(g.double().cpu().numpy(), a.double().cpu().numpy(), [(0, R)])
+    for got in (wide, narrow):
+        check(got[0], *want["w"], False, "grad_w")
+        check(got[1], *want["b"], False, "grad_bias")
