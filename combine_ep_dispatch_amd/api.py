@@ -888,7 +888,8 @@ def expert_linear_backward(grad_y, w, handle, p=None, stream=None):
 def expert_linear_backward_weights(grad_y, a, handle, dtype=torch.bfloat16, bias=False, stream=None):
     """Gradient of expert_linear w.r.t. its weights -> [E, N, H] of ``dtype``
     (bfloat16 or float32; [1, N, H] for ``handle`` None); with bias -> (grad_w,
-    grad_bias [E, N])."""
+    grad_bias [E, N]).  (ep_expert_linear_backward_weights adds to gradients
+    that are there.)"""
     rows, cap = _expert_rows(handle)
     g, a2 = _flat("grad_y", grad_y), _flat("a", a)
     E = handle.num_experts if handle is not None else 1

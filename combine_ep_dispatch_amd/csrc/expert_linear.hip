@@ -12,7 +12,7 @@ namespace {
 // registers, eight loads of 16 rows by 64 bytes ahead, and add their sums in LDS
 // in a fixed order.  16 rows of 7168 to 4096, gated: 16.5 us (3.6 TB/s, bounded by
 // the latency of few loads a wave), against 23 in 64 x 64 tiles, which leave half of
-// the CUs idle; 7 rows of 2048 to 7168: 9.4.  Where tiles fill the chip they are
+// the CUs idle; 7 rows of 2048 to 7168: 10.6.  Where tiles fill the chip they are
 // faster (1 token of 8 of 256 experts: 73 against 88 us; 128 tokens 2090 against 2900).
 constexpr int kFewWaves = 8;
 
@@ -126,7 +126,9 @@ __global__ __launch_bounds__(kFewWaves* kWave, 4) void linear_few(const LinearAr
 //   128 x 256              2450      2512       2606       2656        3655        15890
 //   192 x 256              2414      2469       2671       2749       *3016        15510
 //   256 x 256              2531      2652       2880       2969        3216       *13230
-// and for one matrix of the same sizes (its rows), where few tiles are idle CUs:
+// With popular experts (1.2 in Zipf's law) as the rule picks: 512 tokens 2350 us and
+// 2165 evenly, 2048 3080 and 2475, 4096 3680 and 2976.
+// And for one matrix of the same sizes (its rows), where few tiles are idle CUs:
 //   rows                  16    64   128   256   384   512   768  1024  2048
 //   few rows           *16.2          109   214         425         847  1688
 //   64 x 64, 2 groups   23.2 *24.7 *24.9 *26.0  46.6  48.4  70.4

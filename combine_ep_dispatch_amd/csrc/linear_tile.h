@@ -27,7 +27,7 @@
 // TFLOP/s; the matrix unit is busy 84% of the time, at 1.4 GHz: the card's power
 // limit).  With 256 experts of 7168 to 4096 (gated) the weights stream in at 7.1
 // TB/s where an expert has few rows; at 128 rows an expert both bounds meet (5.3
-// TB/s, 650 TFLOP/s, 1.3 GHz); at 1024 rows 1180 TFLOP/s.  Measured without gain:
+// TB/s, 650 TFLOP/s, 1.4 to 1.5 GHz); at 1024 rows 1100 to 1200 TFLOP/s (by the card).  Measured without gain:
 // half a tile's products where an expert's last rows fit that (3% at 128 rows, but
 // tiles that drift apart lose their shared lines in L2: 14.6 against 13.0 ms at 1024
 // rows), four waves of 128 x 128, all of a stage's fragments read at once,
@@ -105,7 +105,8 @@ __device__ __forceinline__ void span_of_one(const int32_t* expert_rows, int e, i
 
 // The gate's sigmoid s = 1 / (1 + exp(-g)) as two factors s1 s2, and n = 1 - s,
 // each without cancellation.  (Two, each with half the exponent, so that s
-// keeps its accuracy below 2^-126, where a large g or d makes it count.)
+// keeps its accuracy below 2^-126, where a large u or d makes it count: to g =
+// -174, where each factor ends.)
 struct Gate {
   float s1, s2, n;
 };
@@ -142,8 +143,11 @@ __device__ __forceinline__ void copy_piece(Rsrc src, uint8_t* dst, uint32_t lane
   else copy16(src, dst, lane_off, off);
 }
 
-// A lane offset past the end of every operand's buffer resource (at most 2^25
-// bytes): loads from there give 0.
+// A lane offset past the end of every buffer resource: loads from there give 0,
+// and stores are dropped.  Needs resources of at most 2^31 bytes, and offsets added
+// to it of less.  Here a tile's rows reach 2^26 bytes (256 rows of 2 x 65536 bf16
+// channels of p, or of 65536 binary32 gradients), linear_few's matrix of one expert
+// nearly 2^31.
 constexpr uint32_t kNone = 0x80000000u;
 
 // WM x WN: the tile's waves; XS, RS: stages of X and of R kept; PER: workgroups
@@ -650,7 +654,9 @@ __global__ __launch_bounds__(G* WM* WN* kWave, (G * WM * WN * PER + 3) / 4) void
     // row and store 64 bytes (from the accumulators' layout it would be 8).  What a
     // fragment needs from memory is read before the one before it is stored: a
     // wait for loads is one for the stores ahead of them (4096 rows of 2048 to 7168 with
-    // a residual: 121 against 131 us).  Rows and channels past the
+    // a residual: 121 against 131 us).  Not so an old gradient (g.add), which is read
+    // where it is added: 32 matrices of 7168 x 2048 in binary32 take 1455 us so and 1069
+    // without, where a read of them alone takes some 310.  Rows and channels past the
     // end are past the end of the buffer resources, where nothing is read or written.
     uint8_t* const yb = x_buf(std::integral_constant<int, XS - 1>{}) + wave * 4096;
     const auto y_place = [](uint32_t row, uint32_t piece) { return row * 128 + ((piece ^ (row & 7)) * 16); };
@@ -835,7 +841,9 @@ hipError_t launch_tiles(const LinearArgs& g, hipStream_t stream) {
 
 // What the choice of a tile goes by.  The rows of each expert are on the device;
 // the host knows their number, and for the padded layout no more than the
-// capacity, which stands for some 64 rows at most.
+// capacity, which stands for some 64 rows at most (32 experts of 7168 to 4096, gated,
+// capacity 1024 with 128 rows each: 346 us, and 371 packed; capacity 4096 with 1024
+// rows each: 1816, and 1509 packed).
 struct LinearShape {
   int64_t rows, hit;  // and experts that have any, at most
   int64_t avg;        // rows of an expert
